@@ -263,7 +263,9 @@ def _verify_plain(s):
             less[seq, tok[seq, at]] = row[seq, tok[seq, at]]
         else:
             less = s["q"][seq, at].double()
-        row = torch.where(rejected[:, None], (row - less).clamp(min=0), row)
+        rest = (row - less).clamp(min=0)
+        rejected = rejected & (rest.sum(1) > 0)       # no mass left by rounding: the target row itself
+        row = torch.where(rejected[:, None], rest, row)
     cdf = row.cumsum(1)
     cut = s["u"][:, k].double() * cdf[:, -1]
     nxt = (cdf <= cut[:, None]).sum(1).clamp(max=v - 1)
@@ -416,6 +418,7 @@ def _exact_verify(s):
                 rest[tok[i, j]] = 0.0
             else:
                 rest = np.maximum(rest - q[j], 0.0)
+            rest = rest if rest.any() else p[j]
         total = np.cumsum(rest)
         pick = int(np.searchsorted(total, u[i, k] * total[-1], side="right"))
         count[i], nxt[i] = j, min(pick, v - 1)
