@@ -302,6 +302,195 @@ ssd_status ssd_state_correction(void *y, const float *dt, const float *A, const 
                                 const int32_t *state_out_idx, float *state_out,
                                 const ssd_shape *shape, ssd_dtype dtype, void *hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the scan in its layer and in its verify loop: the short
+ * causal convolution before it, the selective scan with one decay per channel
+ * and state index, the gated RMS norm after it, and the verification of
+ * drafted tokens that yields the accepted index.  Conventions as above (device
+ * pointers, stream order, host-side checks before any launch, no allocation),
+ * except that inputs named with a stride below need not be dense: strides are
+ * in elements, >= 0 (0 repeats a row), and of no account along a dimension of
+ * size 1 or less.  The innermost dimension is always contiguous.  Every
+ * pointer is aligned to its own element; faster variants are taken where
+ * pointers and strides allow 16-byte accesses.
+ * -------------------------------------------------------------------------*/
+
+/* Sizes of ssd_causal_conv_fwd.  batch and seqlen may be 0. */
+typedef struct {
+    int64_t batch;           /* b: independent sequences                          */
+    int64_t seqlen;          /* T: tokens per sequence                            */
+    int64_t channels[3];     /* channels of the outputs, in x's order; the first
+                                is > 0, the others may be 0 (no such output)      */
+    int64_t width;           /* W: taps, 2, 3 or 4                                */
+    int64_t x_batch_stride;
+    int64_t x_token_stride;
+} ssd_conv_shape;
+
+/* Activation codes of ssd_causal_conv_fwd. */
+typedef enum {
+    SSD_ACT_NONE = 0,
+    SSD_ACT_SILU = 1   /* v * sigmoid(v) */
+} ssd_activation;
+
+/* Depthwise causal convolution over tokens, with Ch = the sum of channels:
+ *
+ *     o[b,t,c] = act(bias[c] + sum_{k<W} weight[c,k] * x[b, t-(W-1)+k, c])
+ *
+ * where the W-1 tokens before token 0 are init_state (zeros when absent).
+ * The outputs are x's channels in up to three dense tensors, so that a
+ * projection's rows [... | x | B | C | ...] turn into the dense x, B and C
+ * that ssd_chunk_scan_fwd reads (views [b,T,H,P] and [b,T,G,N]).
+ *
+ *   x             [b,T,Ch]     dtype  strided (a slice of a projection's rows)
+ *   weight        [Ch,W]       fp32   the last tap meets the current token
+ *   bias          [Ch]         fp32   NULL = none
+ *   init_state    [b,W-1,Ch]   dtype  the inputs before token 0, oldest first;
+ *                                     NULL = zeros
+ *   out0..out2    [b,T,channels[i]]   dtype; NULL exactly where channels[i] is 0
+ *                                     (sums in fp32, rounded once)
+ *   final_state   [b,W-1,Ch]   dtype  the last W-1 inputs (reaching back into
+ *                                     init_state when T < W-1); NULL = not
+ *                                     returned; may be init_state itself
+ *   state_out_idx [b]          int32  accepted index j_b in [-1, T-1]; NULL = none
+ *   state_out     [b,W-1,Ch]   dtype  the W-1 inputs ending at token j_b (-1:
+ *                                     init_state); non-NULL exactly when
+ *                                     state_out_idx is
+ * With a padded batch, j_b = length - 1 gives each sequence's own state.
+ * One kernel, no workspace.  Ch <= 2^20. */
+ssd_status ssd_causal_conv_fwd(const void *x, const float *weight, const float *bias,
+                               const void *init_state, int activation,
+                               void *out0, void *out1, void *out2, void *final_state,
+                               const int32_t *state_out_idx, void *state_out,
+                               const ssd_conv_shape *shape, ssd_dtype dtype, void *hip_stream);
+
+/* Sizes of ssd_selective_scan_fwd.  batch and seqlen may be 0. */
+typedef struct {
+    int64_t batch;      /* b                                                    */
+    int64_t seqlen;     /* T                                                    */
+    int64_t channels;   /* Dm: channels, a multiple of ngroups                  */
+    int64_t dstate;     /* N: 8, 16, 32 or 64                                   */
+    int64_t ngroups;    /* G: B/C groups; channel d reads group d*G/Dm          */
+    int64_t u_batch_stride, u_token_stride;
+    int64_t delta_batch_stride, delta_token_stride;
+    int64_t z_batch_stride, z_token_stride;
+    int64_t B_batch_stride, B_token_stride;
+    int64_t C_batch_stride, C_token_stride;
+} ssd_selective_shape;
+
+/* The selective scan with one decay per channel and state index:
+ *
+ *     s[b,t,d]   = delta + delta_bias[d], through softplus when delta_softplus
+ *     h_t[d][n]  = exp(s * A[d][n]) * h_{t-1}[d][n] + s * u[b,t,d] * B[b,t,g,n]
+ *     y[b,t,d]   = (sum_n C[b,t,g,n] * h_t[d][n] + D[d] * u[b,t,d]) * silu(z[b,t,d])
+ *
+ * with h_{-1} = init_state (zeros when absent); silu(z) is left out without z.
+ *
+ *   u, delta      [b,T,Dm]    dtype  strided
+ *   A             [Dm,N]      fp32   (<= 0; values > 0 are computed as given)
+ *   B, C          [b,T,G,N]   dtype  strided by batch and token; a token's G*N
+ *                                    values are contiguous
+ *   D             [Dm]        fp32   NULL = no skip term
+ *   z             [b,T,Dm]    dtype  strided; NULL = no gate
+ *   delta_bias    [Dm]        fp32   NULL = none
+ *   init_state    [b,Dm,N]    fp32   NULL = zeros
+ *   y             [b,T,Dm]    dtype  dense, rounded once from fp32
+ *   final_state   [b,Dm,N]    fp32   NULL = not returned; may be init_state itself
+ *   state_out_idx [b]         int32  accepted index j_b in [-1, T-1]; NULL = none
+ *   state_out     [b,Dm,N]    fp32   the state after token j_b (-1: init_state);
+ *                                    non-NULL exactly when state_out_idx is
+ *   workspace     16-byte aligned, ssd_selective_scan_workspace_bytes(...) bytes,
+ *                 contents on entry ignored; may be NULL when that is 0
+ * A and every state are 16-byte aligned.  Calls of few sequences and channels
+ * share a long sequence out over the GPU (this needs the workspace); the choice
+ * depends on the sizes alone. */
+ssd_status ssd_selective_scan_fwd(const void *u, const void *delta, const float *A,
+                                  const void *B, const void *C, const float *D,
+                                  const void *z, const float *delta_bias, int delta_softplus,
+                                  const float *init_state, void *y, float *final_state,
+                                  const int32_t *state_out_idx, float *state_out,
+                                  const ssd_selective_shape *shape, ssd_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace ssd_selective_scan_fwd needs; 0 also when the arguments
+ * are invalid (ssd_last_error() says why). */
+size_t ssd_selective_scan_workspace_bytes(const ssd_selective_shape *shape, ssd_dtype dtype);
+
+/* Sizes of ssd_gated_norm_fwd.  rows may be 0. */
+typedef struct {
+    int64_t rows;
+    int64_t dim;            /* elements per row, a multiple of ngroups           */
+    int64_t ngroups;        /* each row is normalised in ngroups equal parts     */
+    int64_t x_row_stride;
+    int64_t z_row_stride;
+} ssd_norm_shape;
+
+/* RMS norm with a gate, the step between the scan and the output projection:
+ *
+ *     norm_before_gate == 0:  v = x * silu(z);  out = v / rms(v) * weight
+ *     norm_before_gate != 0:  out = x / rms(x) * weight * silu(z)
+ *
+ * with rms(v) = sqrt(mean(v^2) + eps) over each of the row's ngroups parts
+ * (statistics in fp32).  Without z: out = x / rms(x) * weight.
+ *
+ *   x       [rows,dim]  dtype  strided by row
+ *   z       [rows,dim]  dtype  strided by row; NULL = no gate
+ *   weight  [dim]       fp32   NULL = ones
+ *   out     [rows,dim]  dtype  dense; may be x or z itself where that is dense
+ *   eps     >= 0 and finite
+ * One kernel, no workspace.  dim <= 2^20. */
+ssd_status ssd_gated_norm_fwd(const void *x, const void *z, const float *weight, void *out,
+                              float eps, int norm_before_gate,
+                              const ssd_norm_shape *shape, ssd_dtype dtype, void *hip_stream);
+
+/* Sizes of ssd_verify_drafts.  batch and drafts may be 0. */
+typedef struct {
+    int64_t batch;       /* b: sequences                                         */
+    int64_t drafts;      /* K: drafted tokens per sequence (at most)             */
+    int64_t vocab;       /* V: probabilities per row                             */
+    int64_t target_batch_stride, target_row_stride;
+    int64_t draft_batch_stride, draft_row_stride;
+} ssd_verify_shape;
+
+/* Verification of drafted tokens against the target's probabilities, by the
+ * rejection rule that leaves the target's distribution unchanged.  For each
+ * sequence with m = draft_lens[b] drafts (K without draft_lens):
+ *
+ *     n    = the first i < m with  u_i * q_i(tok_i) >= p_i(tok_i)   (m if none)
+ *     r(v) = max(p_n(v) - q_n(v), 0)  for n < m;   p_m(v)  for n = m
+ *     next = the smallest v with  r(0) + ... + r(v) > u_K * sum(r)
+ *
+ * u_i = uniforms[b,i] and u_K = uniforms[b,K] lie in [0,1).  A row need not
+ * sum to 1: the last line normalises by r's own sum.  Products and sums are in
+ * fp64 in a fixed order, so equal inputs give equal tokens.  Without
+ * draft_probs every q_i is 1 at tok_i and 0 elsewhere (looked-up drafts).
+ * Where rounding left r without mass, p_n takes its place; a row without mass
+ * gives V-1; NaN and negative probabilities count as no mass.
+ *
+ *   target_probs  [b,K+1,V]  dtype  strided; row i judges draft i
+ *   draft_probs   [b,K,V]    dtype  strided; NULL = as above
+ *   draft_tokens  [b,K]      int32  a token outside [0,V) is never accepted
+ *                                   (and takes nothing from p without
+ *                                   draft_probs); may be NULL when K is 0
+ *   draft_lens    [b]        int32  clamped to [0,K]; NULL = K
+ *   uniforms      [b,K+1]    fp32
+ *   n_accepted    [b]        int32  n: also the state_out_idx of a scan over
+ *                                   [last token, drafts], whose index 0 is the
+ *                                   last token that was already accepted
+ *   next_token    [b]        int32
+ *   tokens        [b,K+1]    int32  the n accepted drafts, next, then -1; NULL =
+ *                                   not returned
+ *   workspace     16-byte aligned, ssd_verify_workspace_bytes(...) bytes,
+ *                 contents on entry ignored; may be NULL when that is 0 */
+ssd_status ssd_verify_drafts(const void *target_probs, const void *draft_probs,
+                             const int32_t *draft_tokens, const int32_t *draft_lens,
+                             const float *uniforms, int32_t *n_accepted, int32_t *next_token,
+                             int32_t *tokens, const ssd_verify_shape *shape, ssd_dtype dtype,
+                             void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace ssd_verify_drafts needs; 0 also when the arguments are
+ * invalid (ssd_last_error() says why). */
+size_t ssd_verify_workspace_bytes(const ssd_verify_shape *shape, ssd_dtype dtype);
+
 /* Static description of a status code. */
 const char *ssd_status_string(ssd_status status);
 

@@ -1,4 +1,5 @@
-"""Python binding of libssd, the MI355X (gfx950) SSD chunked-scan forward.
+"""Python binding of libssd, the MI355X (gfx950) SSD chunked-scan forward and
+the operators around it.
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libssd.so`` (built from ``csrc/`` by ``build.py``).  torch
@@ -16,7 +17,9 @@ import os
 __all__ = [
     "SsdError", "ssd_abi_version", "ssd_status_string", "ssd_last_error", "ssd_workspace_bytes",
     "ssd_get_workspace_layout", "ssd_select_path", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_ex",
-    "ssd_chunk_scan_fwd_noalloc", "ssd_state_correction", "SSD_NOALLOC_SCRATCH_BYTES", "workspace_views", "library_path", "SSD_PATH_AUTO", "SSD_PATH_ONE_CHUNK", "SSD_PATH_SINGLE_PASS",
+    "ssd_chunk_scan_fwd_noalloc", "ssd_state_correction", "ssd_causal_conv_fwd", "ssd_selective_scan_fwd",
+    "ssd_selective_scan_workspace_bytes", "ssd_gated_norm_fwd", "ssd_verify_drafts", "ssd_verify_workspace_bytes",
+    "SSD_NOALLOC_SCRATCH_BYTES", "workspace_views", "library_path", "SSD_PATH_AUTO", "SSD_PATH_ONE_CHUNK", "SSD_PATH_SINGLE_PASS",
     "SSD_PATH_CHUNK_PARALLEL",
 ]
 
@@ -48,6 +51,27 @@ class ssd_workspace_layout(ctypes.Structure):
                 ("dt_decay_offset", ctypes.c_size_t), ("states_offset", ctypes.c_size_t),
                 ("prev_offset", ctypes.c_size_t), ("hj_offset", ctypes.c_size_t),
                 ("total_bytes", ctypes.c_size_t), ("nchunks", ctypes.c_int64)]
+
+
+class ssd_conv_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64 * 3),
+                ("width", ctypes.c_int64), ("x_batch_stride", ctypes.c_int64), ("x_token_stride", ctypes.c_int64)]
+
+
+class ssd_selective_shape(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in (
+        "batch", "seqlen", "channels", "dstate", "ngroups", "u_batch_stride", "u_token_stride",
+        "delta_batch_stride", "delta_token_stride", "z_batch_stride", "z_token_stride",
+        "B_batch_stride", "B_token_stride", "C_batch_stride", "C_token_stride")]
+
+
+class ssd_norm_shape(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("rows", "dim", "ngroups", "x_row_stride", "z_row_stride")]
+
+
+class ssd_verify_shape(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in ("batch", "drafts", "vocab", "target_batch_stride",
+                                              "target_row_stride", "draft_batch_stride", "draft_row_stride")]
 
 
 class SsdError(RuntimeError):
@@ -90,6 +114,22 @@ def _load():
     lib.ssd_chunk_scan_fwd_noalloc.restype = i32
     lib.ssd_state_correction.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, shp, i32, vp]
     lib.ssd_state_correction.restype = i32
+    lib.ssd_causal_conv_fwd.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, ctypes.POINTER(ssd_conv_shape),
+                                        i32, vp]
+    lib.ssd_causal_conv_fwd.restype = i32
+    sel = ctypes.POINTER(ssd_selective_shape)
+    lib.ssd_selective_scan_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, sel, i32, vp, sz,
+                                           vp]
+    lib.ssd_selective_scan_fwd.restype = i32
+    lib.ssd_selective_scan_workspace_bytes.argtypes = [sel, i32]
+    lib.ssd_selective_scan_workspace_bytes.restype = sz
+    lib.ssd_gated_norm_fwd.argtypes = [vp, vp, vp, vp, ctypes.c_float, i32, ctypes.POINTER(ssd_norm_shape), i32, vp]
+    lib.ssd_gated_norm_fwd.restype = i32
+    ver = ctypes.POINTER(ssd_verify_shape)
+    lib.ssd_verify_drafts.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ver, i32, vp, sz, vp]
+    lib.ssd_verify_drafts.restype = i32
+    lib.ssd_verify_workspace_bytes.argtypes = [ver, i32]
+    lib.ssd_verify_workspace_bytes.restype = sz
     lib.ssd_status_string.argtypes = [i32]
     lib.ssd_status_string.restype = ctypes.c_char_p
     lib.ssd_last_error.argtypes = []
@@ -138,12 +178,12 @@ def ssd_select_path(shape: ssd_shape, chunk_size: int, dtype: int) -> int:
     return path
 
 
-def _dtype_code(torch, t) -> int:
+def _dtype_code(torch, t, name="x") -> int:
     if t.dtype == torch.bfloat16:
         return SSD_DTYPE_BF16
     if t.dtype == torch.float32:
         return SSD_DTYPE_F32
-    raise TypeError(f"x must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
 def _ptr(t):
@@ -321,6 +361,329 @@ def _run(x, dt, A, B, C, D, init_state, chunk_size, state_out_idx, y, final_stat
     _check(lib.ssd_chunk_scan_fwd_ex(*args, int(path), arr, n, ctypes.byref(count), names))
     used = min(count.value, n - 1) if n > 0 else 0
     return y, final_state, state_out, [names[k].decode() for k in range(used)]
+
+
+# ------------------------------------------------ operators around the scan
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _strided(name, t, shape, dtype, device, inner=1):
+    """Checks a tensor argument whose leading dimensions may be strided and
+    whose last `inner` dimensions are contiguous; returns its strides."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    st = t.stride()
+    want = 1
+    for k in range(1, inner + 1):
+        if st[-k] != want and t.shape[-k] > 1 and t.numel() > 0:
+            raise ValueError(f"{name} must be contiguous in its last {inner} dimension(s)" if inner > 1
+                             else f"{name} must be contiguous in its last dimension")
+        want *= t.shape[-k]
+    return st
+
+
+def _scope(torch, t, stream):
+    """What a call on tensor t has to run inside: t's device and, where one is
+    given, `stream` (a raw handle), so that tensors made by the call belong to
+    the stream that uses them; None where both are current already."""
+    if not t.is_cuda:
+        raise ValueError(f"tensors must be on a GPU device, got {t.device}")
+    if stream is None:
+        return None if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+    if stream == 0:
+        return torch.cuda.stream(torch.cuda.default_stream(t.device))
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device))
+
+
+def _raw_stream(torch, device):
+    return torch.cuda.current_stream(device).cuda_stream or None
+
+
+def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, state_out_idx=None, *, split=None, activation="silu",
+                        out=None, final_state=None, return_final_state: bool = True, state_out=None, stream=None):
+    """Depthwise causal convolution over tokens (see ssd_causal_conv_fwd in
+    include/ssd.h).
+
+    x [b,T,Ch] bf16|fp32 (batch and token strides free, e.g. a slice of a
+    projection's output), weight [Ch,W] fp32 (W 2..4), bias [Ch] fp32 or None,
+    init_state [b,W-1,Ch] like x or None, state_out_idx [b] int32 or None;
+    activation "silu" or None.  With `split` (up to three sizes adding up to
+    Ch) the outputs are that many dense tensors [b,T,size], else one.
+    `out`, a tensor or with `split` a sequence of them, final_state (may be
+    init_state itself) and state_out are allocated when not given.  Returns
+    (out, final_state or None, state_out or None); out is a tuple with
+    `split`.  Errors as for ssd_chunk_scan_fwd.
+    """
+    import torch
+
+    if x.dim() != 3 or weight.dim() != 2:
+        raise ValueError("x must be [b,T,Ch] and weight [Ch,W]")
+    scope = _scope(torch, x, stream) if x.is_cuda else None
+    if scope is not None:
+        with scope:
+            return ssd_causal_conv_fwd(x, weight, bias, init_state, state_out_idx, split=split, activation=activation,
+                                       out=out, final_state=final_state, return_final_state=return_final_state,
+                                       state_out=state_out)
+    b, T, ch = x.shape
+    w = weight.shape[1]
+    code, dtype, dev = _dtype_code(torch, x), x.dtype, x.device
+    st = _strided("x", x, x.shape, dtype, dev)
+    _expect("weight", weight, (ch, w), torch.float32, dev)
+    if activation not in (None, "silu"):
+        raise ValueError(f"activation must be 'silu' or None, got {activation!r}")
+    sizes = [ch] if split is None else [int(k) for k in split]
+    if not 1 <= len(sizes) <= 3 or min(sizes) <= 0 or sum(sizes) != ch:
+        raise ValueError(f"split must be one to three positive sizes adding up to {ch}, got {split}")
+    held = (b, w - 1, ch)
+    if bias is not None:
+        _expect("bias", bias, (ch,), torch.float32, dev)
+    if init_state is not None:
+        _expect("init_state", init_state, held, dtype, dev)
+    if state_out_idx is not None:
+        _expect("state_out_idx", state_out_idx, (b,), torch.int32, dev)
+    elif state_out is not None:
+        raise ValueError("state_out needs state_out_idx")
+    if out is None:
+        outs = None
+    else:
+        outs = [out] if split is None else list(out)
+        if len(outs) != len(sizes):
+            raise ValueError(f"out must hold {len(sizes)} tensors, got {len(outs)}")
+        for k, (o, n) in enumerate(zip(outs, sizes)):
+            _expect("out" if split is None else f"out[{k}]", o, (b, T, n), dtype, dev)
+    if final_state is not None:
+        _expect("final_state", final_state, held, dtype, dev)
+    if state_out is not None:
+        _expect("state_out", state_out, held, dtype, dev)
+    if not x.is_cuda:
+        raise ValueError(f"tensors must be on a GPU device, x is on {dev}")
+    lib = _load()
+    if outs is None:
+        outs = [torch.empty((b, T, n), dtype=dtype, device=dev) for n in sizes]
+    if final_state is None and return_final_state:
+        final_state = torch.empty(held, dtype=dtype, device=dev)
+    if state_out is None and state_out_idx is not None:
+        state_out = torch.empty(held, dtype=dtype, device=dev)
+    pad = [0] * (3 - len(sizes))
+    shape = ssd_conv_shape(b, T, (ctypes.c_int64 * 3)(*sizes, *pad), w, st[0], st[1])
+    _check(lib.ssd_causal_conv_fwd(_addr(x), _addr(weight), _addr(bias), _addr(init_state),
+                                   1 if activation == "silu" else 0, *[_addr(o) for o in outs], *[None for _ in pad],
+                                   _addr(final_state), _addr(state_out_idx), _addr(state_out), ctypes.byref(shape),
+                                   code, _raw_stream(torch, dev)))
+    return (outs[0] if split is None else tuple(outs)), final_state, state_out
+
+
+def ssd_selective_scan_workspace_bytes(shape: ssd_selective_shape, dtype: int) -> int:
+    return int(_load().ssd_selective_scan_workspace_bytes(ctypes.byref(shape), int(dtype)))
+
+
+def ssd_selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, init_state=None, state_out_idx=None, *,
+                           delta_softplus: bool = False, y=None, final_state=None, return_final_state: bool = True,
+                           state_out=None, workspace=None, stream=None):
+    """Selective scan with one decay per channel and state index (see
+    ssd_selective_scan_fwd in include/ssd.h).
+
+    u, delta, z [b,T,Dm] bf16|fp32 (batch and token strides free), A [Dm,N]
+    fp32, B, C [b,T,G,N] like u (strides free by batch and token), D and
+    delta_bias [Dm] fp32 or None, z None for no gate, init_state [b,Dm,N] fp32
+    or None, state_out_idx [b] int32 or None.  Outputs and the workspace are
+    allocated when not given; final_state may be init_state itself.  Returns
+    (y, final_state or None, state_out or None).  Errors as for
+    ssd_chunk_scan_fwd.
+    """
+    import torch
+
+    if u.dim() != 3 or A.dim() != 2 or B.dim() != 4:
+        raise ValueError("u must be [b,T,Dm], A [Dm,N] and B, C [b,T,G,N]")
+    scope = _scope(torch, u, stream) if u.is_cuda else None
+    if scope is not None:
+        with scope:
+            return ssd_selective_scan_fwd(u, delta, A, B, C, D, z, delta_bias, init_state, state_out_idx,
+                                          delta_softplus=delta_softplus, y=y, final_state=final_state,
+                                          return_final_state=return_final_state, state_out=state_out,
+                                          workspace=workspace)
+    f32 = torch.float32
+    b, T, ch = u.shape
+    G, N = B.shape[2], B.shape[3]
+    code, dtype, dev = _dtype_code(torch, u, "u"), u.dtype, u.device
+    su = _strided("u", u, u.shape, dtype, dev)
+    sd = _strided("delta", delta, u.shape, dtype, dev)
+    sz = _strided("z", z, u.shape, dtype, dev) if z is not None else (0, 0)
+    sb = _strided("B", B, (b, T, G, N), dtype, dev, 2)
+    sc = _strided("C", C, (b, T, G, N), dtype, dev, 2)
+    _expect("A", A, (ch, N), f32, dev)
+    if D is not None:
+        _expect("D", D, (ch,), f32, dev)
+    if delta_bias is not None:
+        _expect("delta_bias", delta_bias, (ch,), f32, dev)
+    state = (b, ch, N)
+    if init_state is not None:
+        _expect("init_state", init_state, state, f32, dev)
+    if state_out_idx is not None:
+        _expect("state_out_idx", state_out_idx, (b,), torch.int32, dev)
+    elif state_out is not None:
+        raise ValueError("state_out needs state_out_idx")
+    if y is not None:
+        _expect("y", y, u.shape, dtype, dev)
+    if final_state is not None:
+        _expect("final_state", final_state, state, f32, dev)
+    if state_out is not None:
+        _expect("state_out", state_out, state, f32, dev)
+    if workspace is not None:
+        _expect("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+    if not u.is_cuda:
+        raise ValueError(f"tensors must be on a GPU device, u is on {dev}")
+    lib = _load()
+    shape = ssd_selective_shape(b, T, ch, N, G, su[0], su[1], sd[0], sd[1], sz[0], sz[1], sb[0], sb[1], sc[0], sc[1])
+    ref = ctypes.byref(shape)
+    ws_bytes = 0
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+    else:
+        ws_bytes = lib.ssd_selective_scan_workspace_bytes(ref, code)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    if y is None:
+        y = torch.empty((b, T, ch), dtype=dtype, device=dev)
+    if final_state is None and return_final_state:
+        final_state = torch.empty(state, dtype=f32, device=dev)
+    if state_out is None and state_out_idx is not None:
+        state_out = torch.empty(state, dtype=f32, device=dev)
+    _check(lib.ssd_selective_scan_fwd(_addr(u), _addr(delta), _addr(A), _addr(B), _addr(C), _addr(D), _addr(z),
+                                      _addr(delta_bias), 1 if delta_softplus else 0, _addr(init_state), _addr(y),
+                                      _addr(final_state), _addr(state_out_idx), _addr(state_out), ref, code,
+                                      _addr(workspace), ws_bytes, _raw_stream(torch, dev)))
+    return y, final_state, state_out
+
+
+def _row_stride(name, t):
+    """The one stride that steps through the rows t[..., :] in order."""
+    if t.dim() == 1 or t.numel() == 0:
+        return t.shape[-1]
+    stride, rows = None, 1
+    for k in range(t.dim() - 2, -1, -1):
+        if t.shape[k] == 1:
+            continue
+        if stride is None:
+            stride = t.stride(k)
+        elif t.stride(k) != stride * rows:
+            raise ValueError(f"the rows of {name} must be one stride apart, got strides {t.stride()}")
+        rows *= t.shape[k]
+    return t.shape[-1] if stride is None else stride
+
+
+def ssd_gated_norm_fwd(x, z=None, weight=None, *, ngroups: int = 1, eps: float = 1e-5, norm_before_gate: bool = False,
+                       out=None, stream=None):
+    """RMS norm with a gate (see ssd_gated_norm_fwd in include/ssd.h).
+
+    x [..., dim] bf16|fp32 and z like it (or None) with their rows one stride
+    apart (e.g. a slice of a projection's output), weight [dim] fp32 or None;
+    each row is normalised in `ngroups` equal parts.  out (dense; may be x or
+    z itself where that is dense) is allocated when not given, and returned.
+    Errors as for ssd_chunk_scan_fwd.
+    """
+    import torch
+
+    if x.dim() < 1:
+        raise ValueError("x must be [..., dim]")
+    scope = _scope(torch, x, stream) if x.is_cuda else None
+    if scope is not None:
+        with scope:
+            return ssd_gated_norm_fwd(x, z, weight, ngroups=ngroups, eps=eps, norm_before_gate=norm_before_gate,
+                                      out=out)
+    code, dtype, dev = _dtype_code(torch, x), x.dtype, x.device
+    dim = x.shape[-1]
+    _strided("x", x, x.shape, dtype, dev)
+    if z is not None:
+        _strided("z", z, x.shape, dtype, dev)
+    if weight is not None:
+        _expect("weight", weight, (dim,), torch.float32, dev)
+    if out is not None:
+        _expect("out", out, x.shape, dtype, dev)
+    if not x.is_cuda:
+        raise ValueError(f"tensors must be on a GPU device, x is on {dev}")
+    lib = _load()
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=dev)
+    shape = ssd_norm_shape(x.numel() // dim if dim else 0, dim, ngroups, _row_stride("x", x),
+                           _row_stride("z", z) if z is not None else 0)
+    _check(lib.ssd_gated_norm_fwd(_addr(x), _addr(z), _addr(weight), _addr(out), eps, 1 if norm_before_gate else 0,
+                                  ctypes.byref(shape), code, _raw_stream(torch, dev)))
+    return out
+
+
+def ssd_verify_workspace_bytes(shape: ssd_verify_shape, dtype: int) -> int:
+    return int(_load().ssd_verify_workspace_bytes(ctypes.byref(shape), int(dtype)))
+
+
+def ssd_verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, draft_lens=None, *, n_accepted=None,
+                      next_token=None, tokens=None, workspace=None, stream=None):
+    """Verification of drafted tokens (see ssd_verify_drafts in
+    include/ssd.h).
+
+    target_probs [b,K+1,V] bf16|fp32 and draft_probs [b,K,V] like it (or None
+    for looked-up drafts), batch and row strides free; draft_tokens [b,K]
+    int32, uniforms [b,K+1] fp32 in [0,1), draft_lens [b] int32 or None.
+    Outputs and the workspace are allocated when not given.  Returns
+    (n_accepted [b], next_token [b], tokens [b,K+1]), all int32: the accepted
+    drafts in `tokens` are followed by the next token, then -1.  n_accepted is
+    also the state_out_idx of a scan over [last token, drafts].  Errors as for
+    ssd_chunk_scan_fwd.
+    """
+    import torch
+
+    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+        raise ValueError("target_probs must be [b,K+1,V]")
+    scope = _scope(torch, target_probs, stream) if target_probs.is_cuda else None
+    if scope is not None:
+        with scope:
+            return ssd_verify_drafts(target_probs, draft_tokens, uniforms, draft_probs, draft_lens,
+                                     n_accepted=n_accepted, next_token=next_token, tokens=tokens,
+                                     workspace=workspace)
+    i32 = torch.int32
+    b, rows, V = target_probs.shape
+    K = rows - 1
+    code, dtype, dev = _dtype_code(torch, target_probs, "target_probs"), target_probs.dtype, target_probs.device
+    st = _strided("target_probs", target_probs, target_probs.shape, dtype, dev)
+    sd = _strided("draft_probs", draft_probs, (b, K, V), dtype, dev) if draft_probs is not None else (0, 0)
+    _expect("draft_tokens", draft_tokens, (b, K), i32, dev)
+    _expect("uniforms", uniforms, (b, rows), torch.float32, dev)
+    if draft_lens is not None:
+        _expect("draft_lens", draft_lens, (b,), i32, dev)
+    if n_accepted is not None:
+        _expect("n_accepted", n_accepted, (b,), i32, dev)
+    if next_token is not None:
+        _expect("next_token", next_token, (b,), i32, dev)
+    if tokens is not None:
+        _expect("tokens", tokens, (b, rows), i32, dev)
+    if workspace is not None:
+        _expect("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+    if not target_probs.is_cuda:
+        raise ValueError(f"tensors must be on a GPU device, target_probs is on {dev}")
+    lib = _load()
+    shape = ssd_verify_shape(b, K, V, st[0], st[1], sd[0], sd[1])
+    ref = ctypes.byref(shape)
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+    else:
+        ws_bytes = lib.ssd_verify_workspace_bytes(ref, code)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    if n_accepted is None:
+        n_accepted = torch.empty(b, dtype=i32, device=dev)
+    if next_token is None:
+        next_token = torch.empty(b, dtype=i32, device=dev)
+    if tokens is None:
+        tokens = torch.empty((b, rows), dtype=i32, device=dev)
+    _check(lib.ssd_verify_drafts(_addr(target_probs), _addr(draft_probs), _addr(draft_tokens), _addr(draft_lens),
+                                 _addr(uniforms), _addr(n_accepted), _addr(next_token), _addr(tokens), ref, code,
+                                 _addr(workspace), ws_bytes, _raw_stream(torch, dev)))
+    return n_accepted, next_token, tokens
 
 
 def workspace_views(workspace, shape: ssd_shape, chunk_size: int, dtype: int):

@@ -43,6 +43,27 @@ __device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2
 // below the fp32 normal range flush to zero).
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// v sigmoid(v); the hardware reciprocal is good to one unit in the last place.
+// A large negative v gives -0 (the exponential overflows to +inf).
+__device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.0f + exp2_hw(-v * kLog2e)); }
+// log(1 + e^x) with full relative accuracy, also where it is small: with e =
+// exp(-|x|) in (0, 1] and r = e / (2 + e) in (0, 1/3], log(1 + e) = 2 atanh(r)
+// = 2 r (1 + r^2/3 + r^4/5 + ...); eight terms leave (1/9)^8 / 17 = 1.4e-9.
+__device__ __forceinline__ float softplus(float x) {
+    const float e = exp2_hw(-fabsf(x) * kLog2e);
+    const float r = e * __builtin_amdgcn_rcpf(2.0f + e);
+    const float q = r * r;
+    float s = 1.0f / 15.0f;
+    s = fmaf(s, q, 1.0f / 13.0f);
+    s = fmaf(s, q, 1.0f / 11.0f);
+    s = fmaf(s, q, 1.0f / 9.0f);
+    s = fmaf(s, q, 1.0f / 7.0f);
+    s = fmaf(s, q, 1.0f / 5.0f);
+    s = fmaf(s, q, 1.0f / 3.0f);
+    s = fmaf(s, q, 1.0f);
+    return fmaxf(x, 0.0f) + 2.0f * r * s;
+}
+
 __device__ __forceinline__ float to_f32(bf16 v) { return (float)v; }
 __device__ __forceinline__ float to_f32(float v) { return v; }
 

@@ -75,4 +75,68 @@ hipError_t launch_empty_sequence(const Params &p, hipStream_t stream);
 // state_out_idx; updates y and state_out in place.
 hipError_t launch_state_correction(const Params &p, Elem e, hipStream_t stream);
 
+// ------------------------------------------------- operators around the scan
+// Short causal convolution (ssd_causal_conv_fwd); pointers and strides as in
+// include/ssd.h.
+struct ConvParams {
+    const void *x;             // [b,T,Ch] strided
+    const float *weight;       // [Ch,W]
+    const float *bias;         // [Ch] or null
+    const void *init_state;    // [b,W-1,Ch] or null
+    void *out[3];              // [b,T,channels[i]]
+    void *final_state;         // [b,W-1,Ch] or null
+    const int32_t *state_out_idx;
+    void *state_out;           // [b,W-1,Ch] or null
+    int64_t batch, seqlen;
+    int64_t x_bs, x_ts;        // batch and token stride
+    int channels[3], total;    // outputs' channels and their sum
+    int width;
+    int silu;
+};
+hipError_t launch_causal_conv(const ConvParams &p, Elem e, hipStream_t stream);
+
+// Selective scan with one decay per channel and state index
+// (ssd_selective_scan_fwd).
+struct SelectiveParams {
+    const void *u, *delta, *B, *C, *z;  // strided; z may be null
+    const float *A;                     // [D,N]
+    const float *D, *delta_bias;        // [D] or null
+    const float *init_state;            // [b,D,N] or null
+    void *y;                            // [b,T,D]
+    float *final_state;                 // [b,D,N] or null
+    const int32_t *state_out_idx;
+    float *state_out;                   // [b,D,N] or null
+    int64_t batch, seqlen;
+    int64_t u_bs, u_ts, delta_bs, delta_ts, z_bs, z_ts, B_bs, B_ts, C_bs, C_ts;
+    int channels, dstate, ngroups;
+    int group_channels;                 // channels / ngroups
+    int softplus;
+};
+hipError_t launch_selective_scan(const SelectiveParams &p, Elem e, hipStream_t stream);
+
+// Gated RMS norm (ssd_gated_norm_fwd).
+struct NormParams {
+    const void *x, *z;         // strided by row; z may be null
+    const float *weight;       // [dim] or null
+    void *out;                 // [rows,dim]
+    int64_t rows, x_rs, z_rs;
+    int dim, ngroups, group_dim;
+    float eps;
+    int norm_before_gate;
+};
+hipError_t launch_gated_norm(const NormParams &p, Elem e, hipStream_t stream);
+
+// Verification of drafted tokens (ssd_verify_drafts).
+struct VerifyParams {
+    const void *target, *draft;  // strided; draft may be null
+    const int32_t *tok;          // [b,K] or null when K is 0
+    const int32_t *lens;         // [b] or null
+    const float *u;              // [b,K+1]
+    int32_t *n_accepted, *next_token, *tokens;  // tokens may be null
+    int64_t batch, vocab;
+    int64_t t_bs, t_rs, d_bs, d_rs;
+    int drafts;
+};
+hipError_t launch_verify_drafts(const VerifyParams &p, Elem e, hipStream_t stream);
+
 }  // namespace ssd

@@ -24,22 +24,18 @@
 #include <mutex>
 #include <string>
 
-#include "ssd.h"
+#include "host_common.hpp"
 #include "kernels.hpp"
+#include "ssd.h"
 
 namespace {
 
 thread_local std::string g_last_error;
 
-ssd_status fail(ssd_status s, const char *fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return s;
-}
+using ssd::fail;
+using ssd::overlaps;
+using ssd::Range;
+using ssd::range;
 
 constexpr size_t kAlign = 256;
 size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -130,20 +126,6 @@ bool path_takes(ssd_path path, const ssd::Params &p, ssd_dtype dtype) {
     }
 }
 
-struct Range {
-    const char *name;
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range(const char *name, const void *p, size_t bytes) {
-    uintptr_t lo = (uintptr_t)p;
-    return Range{name, lo, p ? lo + bytes : lo};
-}
-
-bool overlaps(const Range &a, const Range &b) {
-    return a.lo != a.hi && b.lo != b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
 // Runs the launch sequence, stops at the first failure and records the
 // caller's timing marks after each kernel.
 struct Launcher {
@@ -178,6 +160,16 @@ struct Launcher {
 };
 
 }  // namespace
+
+ssd_status ssd::fail(ssd_status s, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return s;
+}
 
 // Workspace of ssd_chunk_scan_fwd_noalloc: every GPU the library runs on holds
 // its own copy from the time the library's device code is loaded there until
