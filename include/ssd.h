@@ -415,13 +415,13 @@ ssd_status ssd_selective_scan_fwd(const void *u, const void *delta, const float 
  * are invalid (ssd_last_error() says why). */
 size_t ssd_selective_scan_workspace_bytes(const ssd_selective_shape *shape, ssd_dtype dtype);
 
-/* Sizes of ssd_gated_norm_fwd.  rows may be 0. */
+/* Sizes of ssd_gated_norm_fwd.  batch and seqlen may be 0. */
 typedef struct {
-    int64_t rows;
+    int64_t batch, seqlen;  /* b, T: one row per token                           */
     int64_t dim;            /* elements per row, a multiple of ngroups           */
     int64_t ngroups;        /* each row is normalised in ngroups equal parts     */
-    int64_t x_row_stride;
-    int64_t z_row_stride;
+    int64_t x_batch_stride, x_token_stride;
+    int64_t z_batch_stride, z_token_stride;
 } ssd_norm_shape;
 
 /* RMS norm with a gate, the step between the scan and the output projection:
@@ -432,12 +432,12 @@ typedef struct {
  * with rms(v) = sqrt(mean(v^2) + eps) over each of the row's ngroups parts
  * (statistics in fp32).  Without z: out = x / rms(x) * weight.
  *
- *   x       [rows,dim]  dtype  strided by row
- *   z       [rows,dim]  dtype  strided by row; NULL = no gate
- *   weight  [dim]       fp32   NULL = ones
- *   out     [rows,dim]  dtype  dense; may be x or z itself where that is dense
+ *   x       [b,T,dim]  dtype  strided
+ *   z       [b,T,dim]  dtype  strided; NULL = no gate
+ *   weight  [dim]      fp32   NULL = ones
+ *   out     [b,T,dim]  dtype  dense; may be x or z itself where that is dense
  *   eps     >= 0 and finite
- * One kernel, no workspace.  dim <= 2^20. */
+ * One kernel, no workspace.  dim <= 2^20, b*T < 2^31. */
 ssd_status ssd_gated_norm_fwd(const void *x, const void *z, const float *weight, void *out,
                               float eps, int norm_before_gate,
                               const ssd_norm_shape *shape, ssd_dtype dtype, void *hip_stream);

@@ -66,7 +66,8 @@ class ssd_selective_shape(ctypes.Structure):
 
 
 class ssd_norm_shape(ctypes.Structure):
-    _fields_ = [(k, ctypes.c_int64) for k in ("rows", "dim", "ngroups", "x_row_stride", "z_row_stride")]
+    _fields_ = [(k, ctypes.c_int64) for k in (
+        "batch", "seqlen", "dim", "ngroups", "x_batch_stride", "x_token_stride", "z_batch_stride", "z_token_stride")]
 
 
 class ssd_verify_shape(ctypes.Structure):
@@ -561,29 +562,26 @@ def ssd_selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, i
     return y, final_state, state_out
 
 
-def _row_stride(name, t):
-    """The one stride that steps through the rows t[..., :] in order."""
-    if t.dim() == 1 or t.numel() == 0:
-        return t.shape[-1]
-    stride, rows = None, 1
-    for k in range(t.dim() - 2, -1, -1):
-        if t.shape[k] == 1:
-            continue
-        if stride is None:
-            stride = t.stride(k)
-        elif t.stride(k) != stride * rows:
-            raise ValueError(f"the rows of {name} must be one stride apart, got strides {t.stride()}")
-        rows *= t.shape[k]
-    return t.shape[-1] if stride is None else stride
+def _two_levels(name, t, b, T):
+    """The strides of t[..., :] seen as [b,T,dim], where b and T are the
+    products of leading dimensions (b of all but the last of them)."""
+    if t.dim() <= 3:
+        return (0, t.stride(0) if t.dim() == 2 else 0) if t.dim() < 3 else t.stride()[:2]
+    try:
+        return t.view(b, T, t.shape[-1]).stride()[:2]
+    except RuntimeError:
+        raise ValueError(f"{name} of shape {tuple(t.shape)} and strides {t.stride()} cannot be viewed as "
+                         f"[{b}, {T}, {t.shape[-1]}]") from None
 
 
 def ssd_gated_norm_fwd(x, z=None, weight=None, *, ngroups: int = 1, eps: float = 1e-5, norm_before_gate: bool = False,
                        out=None, stream=None):
     """RMS norm with a gate (see ssd_gated_norm_fwd in include/ssd.h).
 
-    x [..., dim] bf16|fp32 and z like it (or None) with their rows one stride
-    apart (e.g. a slice of a projection's output), weight [dim] fp32 or None;
-    each row is normalised in `ngroups` equal parts.  out (dense; may be x or
+    x [dim], [T,dim], [b,T,dim] or more leading dimensions (those before the
+    last two merge into one) bf16|fp32 and z like it or None, batch and token
+    strides free (e.g. a slice of a projection's output); weight [dim] fp32 or
+    None; each row is normalised in `ngroups` equal parts.  out (dense; may be x or
     z itself where that is dense) is allocated when not given, and returned.
     Errors as for ssd_chunk_scan_fwd.
     """
@@ -610,8 +608,11 @@ def ssd_gated_norm_fwd(x, z=None, weight=None, *, ngroups: int = 1, eps: float =
     lib = _load()
     if out is None:
         out = torch.empty(x.shape, dtype=dtype, device=dev)
-    shape = ssd_norm_shape(x.numel() // dim if dim else 0, dim, ngroups, _row_stride("x", x),
-                           _row_stride("z", z) if z is not None else 0)
+    T = x.shape[-2] if x.dim() > 1 else 1
+    b = x.numel() // (T * dim) if T * dim else 0
+    sx = _two_levels("x", x, b, T)
+    sz = _two_levels("z", z, b, T) if z is not None else (0, 0)
+    shape = ssd_norm_shape(b, T, dim, ngroups, sx[0], sx[1], sz[0], sz[1])
     _check(lib.ssd_gated_norm_fwd(_addr(x), _addr(z), _addr(weight), _addr(out), eps, 1 if norm_before_gate else 0,
                                   ctypes.byref(shape), code, _raw_stream(torch, dev)))
     return out

@@ -18,8 +18,9 @@ __global__ __launch_bounds__(kThreads) void gated_norm_kernel(NormParams p) {
     for (int64_t k = blockIdx.x; k < parts; k += gridDim.x) {
         const int64_t row = k / p.ngroups;
         const int c0 = (int)(k - row * p.ngroups) * p.group_dim;
-        const T *x = reinterpret_cast<const T *>(p.x) + row * p.x_rs + c0;
-        const T *z = p.z ? reinterpret_cast<const T *>(p.z) + row * p.z_rs + c0 : nullptr;
+        const int64_t b = row / p.seqlen, t = row - b * p.seqlen;
+        const T *x = reinterpret_cast<const T *>(p.x) + b * p.x_bs + t * p.x_ts + c0;
+        const T *z = p.z ? reinterpret_cast<const T *>(p.z) + b * p.z_bs + t * p.z_ts + c0 : nullptr;
         T *out = reinterpret_cast<T *>(p.out) + row * p.dim + c0;
         float sum = 0.0f;
         for (int i = threadIdx.x; i < p.group_dim; i += kThreads) {

@@ -116,10 +116,11 @@ hipError_t launch_selective_scan(const SelectiveParams &p, Elem e, hipStream_t s
 
 // Gated RMS norm (ssd_gated_norm_fwd).
 struct NormParams {
-    const void *x, *z;         // strided by row; z may be null
+    const void *x, *z;         // [b,T,dim] strided; z may be null
     const float *weight;       // [dim] or null
-    void *out;                 // [rows,dim]
-    int64_t rows, x_rs, z_rs;
+    void *out;                 // [b,T,dim]
+    int64_t rows, seqlen;      // rows = b * T
+    int64_t x_bs, x_ts, z_bs, z_ts;
     int dim, ngroups, group_dim;
     float eps;
     int norm_before_gate;

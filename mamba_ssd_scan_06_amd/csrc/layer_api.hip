@@ -267,35 +267,44 @@ ssd_status ssd_gated_norm_fwd(const void *x, const void *z, const float *weight,
     if (!s) return fail(SSD_ERR_NULL, "shape is NULL");
     ssd_status st = check_dtype(dtype);
     if (st != SSD_OK) return st;
-    if (s->rows < 0) return fail(SSD_ERR_SHAPE, "rows must be >= 0");
+    if (s->batch < 0 || s->seqlen < 0) return fail(SSD_ERR_SHAPE, "batch and seqlen must be >= 0");
     if (s->dim <= 0 || s->ngroups <= 0 || s->dim % s->ngroups != 0)
         return fail(SSD_ERR_SHAPE, "dim (%lld) must be a positive multiple of ngroups (%lld)", (long long)s->dim,
                     (long long)s->ngroups);
-    if (s->dim > kMaxWide || s->rows >= kMaxTokens)
-        return fail(SSD_ERR_UNSUPPORTED, "problem too large (dim <= 2^20, rows < 2^31)");
+    const int64_t rows = product(s->batch, s->seqlen);
+    if (s->dim > kMaxWide || rows < 0 || rows >= kMaxTokens)
+        return fail(SSD_ERR_UNSUPPORTED, "problem too large (dim <= 2^20, batch * seqlen < 2^31)");
     if (!(eps >= 0.0f) || isinf(eps)) return fail(SSD_ERR_ARGS, "eps must be finite and >= 0");
-    const int64_t x_n = extent3(1, 0, s->rows, s->x_row_stride, s->dim),
-                  z_n = z ? extent3(1, 0, s->rows, s->z_row_stride, s->dim) : 0, out_n = product(s->rows, s->dim);
+    const int64_t x_n = extent3(s->batch, s->x_batch_stride, s->seqlen, s->x_token_stride, s->dim),
+                  z_n = z ? extent3(s->batch, s->z_batch_stride, s->seqlen, s->z_token_stride, s->dim) : 0,
+                  out_n = product(rows, s->dim);
     if (x_n < 0 || z_n < 0 || out_n < 0) return fail(SSD_ERR_SHAPE, "a stride is negative or the problem too large");
-    if (s->rows > 0 && (!x || !out)) return fail(SSD_ERR_NULL, "x and out are required");
+    if (rows > 0 && (!x || !out)) return fail(SSD_ERR_NULL, "x and out are required");
     const size_t e = elem_size(dtype);
     const Ptr ptrs[] = {{"x", x, e}, {"z", z, e}, {"weight", weight, 4}, {"out", out, e}};
     if ((st = check_align(ptrs)) != SSD_OK) return st;
-    // An input of the same extent as out is dense, so row r of out is its row r.
+    // In place only where out's rows are the input's own.
+    auto dense = [&](int64_t bs, int64_t ts) {
+        return (s->seqlen == 1 || ts == s->dim) && (s->batch == 1 || bs == s->seqlen * s->dim);
+    };
     const Range o[] = {range("out", out, e * out_n)};
     const Range in[] = {range("x", x, e * x_n), range("z", z, e * z_n), range("weight", weight, 4 * s->dim)};
-    const InPlace allowed[] = {{0, 0}, {0, 1}};
+    const InPlace allowed[] = {{dense(s->x_batch_stride, s->x_token_stride) ? 0 : -1, 0},
+                               {dense(s->z_batch_stride, s->z_token_stride) ? 0 : -1, 1}};
     if ((st = check_alias(o, in, allowed)) != SSD_OK) return st;
-    if (s->rows == 0) return SSD_OK;  // nothing to enqueue
+    if (rows == 0) return SSD_OK;  // nothing to enqueue
 
     ssd::NormParams p = {};
     p.x = x;
     p.z = z;
     p.weight = weight;
     p.out = out;
-    p.rows = s->rows;
-    p.x_rs = used_stride(s->rows, s->x_row_stride);
-    p.z_rs = used_stride(s->rows, s->z_row_stride);
+    p.rows = rows;
+    p.seqlen = s->seqlen;
+    p.x_bs = used_stride(s->batch, s->x_batch_stride);
+    p.x_ts = used_stride(s->seqlen, s->x_token_stride);
+    p.z_bs = used_stride(s->batch, s->z_batch_stride);
+    p.z_ts = used_stride(s->seqlen, s->z_token_stride);
     p.dim = (int)s->dim;
     p.ngroups = (int)s->ngroups;
     p.group_dim = (int)(s->dim / s->ngroups);

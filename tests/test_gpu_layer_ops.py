@@ -350,6 +350,12 @@ def test_norm_shapes_and_in_place():
         torch.cuda.synchronize()
         assert torch.equal(got, want)
     assert ssd.ssd_gated_norm_fwd(x[:0], z[:0], w).shape == (0, 5, 256)
+    # A token range of a padded batch, one row, and four dimensions.
+    assert torch.equal(ssd.ssd_gated_norm_fwd(x[:, 1:4], z[:, 1:4], w), want[:, 1:4])
+    assert torch.equal(ssd.ssd_gated_norm_fwd(x[1, 2], z[1, 2], w), want[1, 2])
+    four = lambda t: t.unflatten(2, (4, 64)).contiguous()
+    assert torch.equal(ssd.ssd_gated_norm_fwd(four(x), four(z), w[:64]).flatten(1, 2),
+                       ssd.ssd_gated_norm_fwd(x.view(3, 20, 64), z.view(3, 20, 64), w[:64]))
     # A zero row keeps its zeros; a NaN row touches no other.
     x = x.clone()
     x[0, 0] = 0

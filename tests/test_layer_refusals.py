@@ -57,10 +57,10 @@ class Scan(Call):
 class Norm(Call):
     name = "ssd_gated_norm_fwd"
 
-    def __init__(self, rows=4, dim=64, G=2, xs=64, zs=64, eps=1e-5):
+    def __init__(self, rows=4, dim=64, G=2, xs=64, zs=64, eps=1e-5, b=1, xb=256, zb=256):
         super().__init__(["x", "z", "weight", "out"],
                          ["x", "z", "weight", "out", "eps", "first", "shape", "dtype", "stream"],
-                         ssd.ssd_norm_shape(rows, dim, G, xs, zs), eps=eps, first=0)
+                         ssd.ssd_norm_shape(b, rows, dim, G, xb, xs, zb, zs), eps=eps, first=0)
 
 
 class Verify(Call):
@@ -87,6 +87,8 @@ class Verify(Call):
     (lambda: Scan(strides=(64,) * 9 + (1 << 60,)), ERR_SHAPE),
     (lambda: Norm(rows=-1), ERR_SHAPE), (lambda: Norm(dim=0), ERR_SHAPE), (lambda: Norm(G=3), ERR_SHAPE),
     (lambda: Norm(dim=(1 << 20) + 2), ERR_UNSUPPORTED), (lambda: Norm(rows=1 << 31), ERR_UNSUPPORTED),
+    (lambda: Norm(b=1 << 20, rows=1 << 11), ERR_UNSUPPORTED), (lambda: Norm(b=-1), ERR_SHAPE),
+    (lambda: Norm(b=1 << 62, rows=4), ERR_UNSUPPORTED),
     (lambda: Norm(xs=-64), ERR_SHAPE), (lambda: Norm(eps=-1.0), ERR_ARGS), (lambda: Norm(eps=float("nan")), ERR_ARGS),
     (lambda: Norm(eps=float("inf")), ERR_ARGS),
     (lambda: Verify(b=-1), ERR_SHAPE), (lambda: Verify(K=-1), ERR_SHAPE), (lambda: Verify(V=0), ERR_SHAPE),
@@ -156,9 +158,10 @@ def test_overlaps(cls, pairs):
     c = Norm()
     c.p["out"] = c.p["x"] + 16
     assert c() == ERR_ALIAS
-    c = Norm(xs=128)
-    c.p["out"] = c.p["x"]                              # out is dense, x is not
-    assert c() == ERR_ALIAS
+    # out is dense, x is not (also where both end at the same byte).
+    for c in (Norm(xs=128), Norm(b=2, rows=3, xs=128, xb=64)):
+        c.p["out"] = c.p["x"]
+        assert c() == ERR_ALIAS
 
 
 def test_index_pairs_activation_and_workspaces():
