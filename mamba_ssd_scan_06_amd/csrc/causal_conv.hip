@@ -14,10 +14,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRun = 32;  // tokens per run
 
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-    T v[VEC];
-};
 
 template <typename T, int W, int VEC>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvParams p) {

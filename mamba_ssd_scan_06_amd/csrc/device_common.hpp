@@ -273,6 +273,13 @@ template <typename T> struct Vec4;
 template <> struct Vec4<bf16> { typedef bf16x4 type; };
 template <> struct Vec4<float> { typedef f32x4 type; };
 
+// N elements moved as one access at any address aligned to one element
+// (gfx950 global loads and stores of up to 16 bytes need no more).
+template <typename T, int N>
+struct __attribute__((packed, aligned(sizeof(T)))) Pack {
+    T v[N];
+};
+
 // Calls f(std::integral_constant<int, I>{}) for I = 0 .. N-1 (unrolled, with
 // compile-time indices, e.g. for register arrays).
 template <typename F, int... I>

@@ -111,7 +111,15 @@ struct SelectiveParams {
     int channels, dstate, ngroups;
     int group_channels;                 // channels / ngroups
     int softplus;
+    // Token ranges (selective_ranges): with more than one, the workspace holds
+    // each range's final state [ranges][b,D,N] (the last slot: a copy of
+    // init_state) and sum of steps [ranges][b,D].
+    int ranges;
+    int64_t range_len;                  // a multiple of the kernel's tile
+    float *range_state, *range_steps;
 };
+// Chooses ranges and range_len from the sizes.
+void selective_ranges(SelectiveParams &p);
 hipError_t launch_selective_scan(const SelectiveParams &p, Elem e, hipStream_t stream);
 
 // Gated RMS norm (ssd_gated_norm_fwd).

@@ -112,6 +112,17 @@ ssd::SelectiveParams selective_params(const ssd_selective_shape *s) {
     return p;
 }
 
+// Byte offsets of the range states and sums of steps in the workspace.
+struct SelectiveWorkspace {
+    size_t steps_off, total;
+};
+SelectiveWorkspace selective_workspace(const ssd::SelectiveParams &p) {
+    if (p.ranges <= 1) return {0, 0};
+    const size_t n = (size_t)p.ranges * p.batch * p.channels;
+    const size_t states = (n * p.dstate * sizeof(float) + 255) / 256 * 256;
+    return {states, states + n * sizeof(float)};
+}
+
 ssd_status check_verify(const ssd_verify_shape *s, ssd_dtype dtype) {
     if (!s) return fail(SSD_ERR_NULL, "shape is NULL");
     ssd_status st = check_dtype(dtype);
@@ -200,7 +211,9 @@ ssd_status ssd_causal_conv_fwd(const void *x, const float *weight, const float *
 
 size_t ssd_selective_scan_workspace_bytes(const ssd_selective_shape *shape, ssd_dtype dtype) {
     if (check_selective(shape, dtype) != SSD_OK) return 0;
-    return 0;
+    ssd::SelectiveParams p = selective_params(shape);
+    ssd::selective_ranges(p);
+    return selective_workspace(p).total;
 }
 
 ssd_status ssd_selective_scan_fwd(const void *u, const void *delta, const float *A, const void *B, const void *C,
@@ -223,7 +236,10 @@ ssd_status ssd_selective_scan_fwd(const void *u, const void *delta, const float 
         return fail(SSD_ERR_ARGS, "state_out and state_out_idx must be given together");
     if (b > 0 && T > 0 && (!u || !delta || !A || !B || !C || !y))
         return fail(SSD_ERR_NULL, "u, delta, A, B, C and y are required");
-    const size_t ws_need = ssd_selective_scan_workspace_bytes(s, dtype);
+    ssd::SelectiveParams p = selective_params(s);
+    ssd::selective_ranges(p);
+    const SelectiveWorkspace ws = selective_workspace(p);
+    const size_t ws_need = ws.total;
     if (ws_need > 0 && !workspace) return fail(SSD_ERR_WORKSPACE, "workspace is NULL");
     if (workspace_bytes < ws_need)
         return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, ws_need);
@@ -243,7 +259,6 @@ ssd_status ssd_selective_scan_fwd(const void *u, const void *delta, const float 
     if ((st = check_alias(o, in, allowed)) != SSD_OK) return st;
     if (b == 0 || (T == 0 && !final_state && !state_out)) return SSD_OK;  // nothing to enqueue
 
-    ssd::SelectiveParams p = selective_params(s);
     p.u = u;
     p.delta = delta;
     p.A = A;
@@ -253,6 +268,10 @@ ssd_status ssd_selective_scan_fwd(const void *u, const void *delta, const float 
     p.z = z;
     p.delta_bias = delta_bias;
     p.softplus = delta_softplus != 0;
+    if (ws_need > 0) {
+        p.range_state = static_cast<float *>(workspace);
+        p.range_steps = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.steps_off);
+    }
     p.init_state = init_state;
     p.y = y;
     p.final_state = final_state;
