@@ -1,10 +1,14 @@
 // Depthwise causal convolution over tokens with the layer's activation and the
 // split into the scan's inputs:
 //     o[t][c] = act(bias[c] + sum_k weight[c][k] x[t-(W-1)+k][c])
-// A thread owns VEC adjacent channels and walks a run of tokens with the last
-// W-1 inputs in registers, so each input is read once (plus W-1 rows per run).
-// Products and sums are in fp32, rounded once on store; the states are raw
-// inputs and never rounded.
+//
+// Every input is needed by W outputs of its own channel only, so the work is
+// one read and one write per element: memory bound.  A thread owns 16 bytes of
+// adjacent channels (fewer at the end of an output) and walks a run of tokens
+// with the last W-1 inputs in registers; a run re-reads W-1 rows of the run
+// before it.  Eight tokens' loads are in flight per thread.  Products and sums
+// are in fp32, rounded once on store; the states are raw inputs and never
+// rounded.
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -12,120 +16,187 @@ namespace ssd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRun = 32;  // tokens per run
+constexpr int kBatchLoads = 8;  // tokens loaded together
 
+// Grid of a launch: threads are numbered channels first, then runs of tokens.
+struct ConvGrid {
+    int vecs[3];      // vectors of VEC channels per output
+    unsigned vecs_all;
+    unsigned work;    // vecs_all * runs
+    int run;          // tokens per run
+};
 
-template <typename T, int W, int VEC>
-__global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvParams p) {
-    using P = Pack<T, VEC>;
-    const int c0 = (blockIdx.x * kThreads + threadIdx.x) * VEC;
-    if (c0 >= p.total) return;
-    const int64_t b = blockIdx.z, T_len = p.seqlen;
-    const T *x = reinterpret_cast<const T *>(p.x) + b * p.x_bs + c0;
-    const int64_t held = (b * (W - 1)) * p.total + c0;
-    // The output this vector of channels belongs to.
-    int o = 0, co = c0, width = p.channels[0];
-    if (co >= width) {
-        co -= width;
-        o = 1;
-        width = p.channels[1];
-        if (co >= width) {
-            co -= width;
-            o = 2;
-            width = p.channels[2];
-        }
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const T *p, int valid) {
+    if (valid == VEC) return *reinterpret_cast<const Pack<T, VEC> *>(p);
+    Pack<T, VEC> r;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) r.v[i] = i < valid ? p[i] : from_f32<T>(0.0f);
+    return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pack(T *p, const Pack<T, VEC> &v, int valid) {
+    if (valid == VEC) {
+        *reinterpret_cast<Pack<T, VEC> *>(p) = v;
+        return;
     }
-    T *out = reinterpret_cast<T *>(o == 0 ? p.out[0] : o == 1 ? p.out[1] : p.out[2]) + b * T_len * width + co;
-
-    P init[W - 1];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) init[k].v[i] = from_f32<T>(0.0f);
-        if (p.init_state && blockIdx.y == 0)
-            init[k] = *reinterpret_cast<const P *>(reinterpret_cast<const T *>(p.init_state) + held +
-                                                   (int64_t)k * p.total);
-    }
-    // Input of token t, which may be one held from before token 0 (t >= 1 - W).
-    // Only run 0 asks for those.
-    auto input = [&](int64_t t) {
-        if (t >= 0) return *reinterpret_cast<const P *>(x + t * p.x_ts);
-        P r = init[0];
-#pragma unroll
-        for (int k = 1; k < W - 1; ++k)
-            if (t + (W - 1) == k) r = init[k];
-        return r;
-    };
-    // Both states come from run 0's threads, which have read init_state by
-    // now: final_state may be the same memory.
-    if (blockIdx.y == 0) {
-        if (p.state_out) {
-            int64_t j = p.state_out_idx[b];
-            j = j < -1 ? -1 : (j > T_len - 1 ? T_len - 1 : j);
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-                *reinterpret_cast<P *>(reinterpret_cast<T *>(p.state_out) + held + (int64_t)k * p.total) =
-                    input(j - (W - 2) + k);
-        }
-        if (p.final_state) {
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-                *reinterpret_cast<P *>(reinterpret_cast<T *>(p.final_state) + held + (int64_t)k * p.total) =
-                    input(T_len - (W - 1) + k);
-        }
-    }
-
-    float w[W][VEC], bias[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        bias[i] = p.bias ? p.bias[c0 + i] : 0.0f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) w[k][i] = p.weight[(int64_t)(c0 + i) * W + k];
-    }
-    for (int64_t t0 = (int64_t)blockIdx.y * kRun; t0 < T_len; t0 += (int64_t)gridDim.y * kRun) {
-        const int64_t t1 = t0 + kRun < T_len ? t0 + kRun : T_len;
-        float hist[W - 1][VEC];
-#pragma unroll
-        for (int k = 0; k < W - 1; ++k) {
-            const P v = input(t0 - (W - 1) + k);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) hist[k][i] = to_f32(v.v[i]);
-        }
-        for (int64_t t = t0; t < t1; ++t) {
-            const P v = *reinterpret_cast<const P *>(x + t * p.x_ts);
-            P r;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float cur = to_f32(v.v[i]);
-                float acc = bias[i];
-#pragma unroll
-                for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], hist[k][i], acc);
-                acc = fmaf(w[W - 1][i], cur, acc);
-#pragma unroll
-                for (int k = 0; k + 1 < W - 1; ++k) hist[k][i] = hist[k + 1][i];
-                hist[W - 2][i] = cur;
-                r.v[i] = from_f32<T>(p.silu ? silu(acc) : acc);
-            }
-            *reinterpret_cast<P *>(out + t * width) = r;
-        }
-    }
+    for (int i = 0; i < VEC; ++i)
+        if (i < valid) p[i] = v.v[i];
 }
 
 template <typename T, int W, int VEC>
+__global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvParams p, ConvGrid gr) {
+    using P = Pack<T, VEC>;
+    const unsigned id = blockIdx.x * kThreads + threadIdx.x;
+    if (id >= gr.work) return;
+    const unsigned run = id / gr.vecs_all;
+    int cv = (int)(id - run * gr.vecs_all);
+    const int64_t b = blockIdx.z, T_len = p.seqlen;
+    // The output this vector of channels belongs to, its first channel there
+    // (co) and overall (c0).
+    int o = 0, base = 0;
+    if (cv >= gr.vecs[0]) {
+        cv -= gr.vecs[0];
+        base = p.channels[0];
+        o = 1;
+        if (cv >= gr.vecs[1]) {
+            cv -= gr.vecs[1];
+            base += p.channels[1];
+            o = 2;
+        }
+    }
+    const int width = o == 0 ? p.channels[0] : o == 1 ? p.channels[1] : p.channels[2];
+    const int co = cv * VEC, c0 = base + co, valid = min(VEC, width - co);
+    const T *x = reinterpret_cast<const T *>(p.x) + b * p.x_bs + c0;
+    T *out = reinterpret_cast<T *>(o == 0 ? p.out[0] : o == 1 ? p.out[1] : p.out[2]) + b * T_len * width + co;
+    const int64_t held = (b * (W - 1)) * p.total + c0;
+    const int64_t t0 = (int64_t)run * gr.run, t1 = min(t0 + gr.run, T_len);
+
+    // The W-1 inputs before the run: hist[k] is token t0 - (W-1) + k.
+    P hist[W - 1];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        const int64_t t = t0 - (W - 1) + k;
+        if (t >= 0) {
+            hist[k] = load_pack<T, VEC>(x + t * p.x_ts, valid);
+        } else if (p.init_state) {  // t >= -(W-1): run 0
+            hist[k] = load_pack<T, VEC>(reinterpret_cast<const T *>(p.init_state) + held + (W - 1 + t) * p.total, valid);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) hist[k].v[i] = from_f32<T>(0.0f);
+        }
+    }
+    // Both states come from run 0's threads, which have read init_state by
+    // now: final_state may be the same memory.
+    if (run == 0 && (p.state_out || p.final_state)) {
+        auto keep = [&](void *to, int64_t last) {  // the W-1 inputs ending at token `last`
+            P v[W - 1];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+                const int64_t t = last - (W - 2) + k;  // >= -(W-1)
+                if (t >= 0) {
+                    v[k] = load_pack<T, VEC>(x + t * p.x_ts, valid);
+                } else {
+                    v[k] = hist[0];
+#pragma unroll
+                    for (int m = 1; m < W - 1; ++m)
+                        if (t + (W - 1) == m) v[k] = hist[m];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k)
+                store_pack<T, VEC>(reinterpret_cast<T *>(to) + held + (int64_t)k * p.total, v[k], valid);
+        };
+        if (p.state_out) {
+            const int64_t j = p.state_out_idx[b];
+            keep(p.state_out, j < -1 ? -1 : (j > T_len - 1 ? T_len - 1 : j));
+        }
+        if (p.final_state) keep(p.final_state, T_len - 1);
+    }
+    if (t0 >= t1) return;
+
+    float w[W][VEC], bias[VEC];
+    if (valid == VEC) {
+        const Pack<float, VEC * W> wv = *reinterpret_cast<const Pack<float, VEC * W> *>(p.weight + (int64_t)c0 * W);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][i] = wv.v[i * W + k];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][i] = i < valid ? p.weight[(int64_t)(c0 + i) * W + k] : 0.0f;
+    }
+    const Pack<float, VEC> bv = p.bias ? load_pack<float, VEC>(p.bias + c0, valid) : Pack<float, VEC>{};
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) bias[i] = bv.v[i];
+
+    // last[k]: the inputs of tokens t - (W-1) + k in fp32.
+    float last[W - 1][VEC];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) last[k][i] = to_f32(hist[k].v[i]);
+    auto token = [&](const P &v) {
+        P r;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const float cur = to_f32(v.v[i]);
+            float acc = bias[i];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], last[k][i], acc);
+            acc = fmaf(w[W - 1][i], cur, acc);
+#pragma unroll
+            for (int k = 0; k + 1 < W - 1; ++k) last[k][i] = last[k + 1][i];
+            last[W - 2][i] = cur;
+            r.v[i] = from_f32<T>(p.silu ? silu(acc) : acc);
+        }
+        return r;
+    };
+    int64_t t = t0;
+    if (valid == VEC)
+        for (; t + kBatchLoads <= t1; t += kBatchLoads) {
+            P v[kBatchLoads];
+#pragma unroll
+            for (int q = 0; q < kBatchLoads; ++q) v[q] = *reinterpret_cast<const P *>(x + (t + q) * p.x_ts);
+#pragma unroll
+            for (int q = 0; q < kBatchLoads; ++q) *reinterpret_cast<P *>(out + (t + q) * width) = token(v[q]);
+        }
+    for (; t < t1; ++t) store_pack<T, VEC>(out + t * width, token(load_pack<T, VEC>(x + t * p.x_ts, valid)), valid);
+}
+
+template <typename T, int W>
 hipError_t run(const ConvParams &p, hipStream_t stream) {
-    const int64_t runs = (p.seqlen + kRun - 1) / kRun;
-    const unsigned gy = (unsigned)std::min<int64_t>(std::max<int64_t>(runs, 1), 65535);
-    const unsigned gx = (unsigned)((p.total / VEC + kThreads - 1) / kThreads);
-    causal_conv_kernel<T, W, VEC><<<dim3(gx, gy, (unsigned)p.batch), kThreads, 0, stream>>>(p);
+    constexpr int VEC = 16 / sizeof(T);
+    ConvGrid gr;
+    int64_t vecs = 0;
+    for (int i = 0; i < 3; ++i) {
+        gr.vecs[i] = (p.channels[i] + VEC - 1) / VEC;
+        vecs += gr.vecs[i];
+    }
+    gr.vecs_all = (unsigned)vecs;
+    // Long runs re-read fewer rows; short ones give more threads.  From 32
+    // tokens down to 8 until the GPU has eight waves per compute unit; and
+    // longer ones where thread numbers would pass 31 bits.
+    int64_t len = 32;
+    while (len > kBatchLoads && vecs * ((p.seqlen + len - 1) / len) * p.batch < 8 * 256 * 64) len /= 2;
+    while (vecs * ((p.seqlen + len - 1) / len) >= ((int64_t)1 << 31) - kThreads) len *= 2;
+    gr.run = (int)len;
+    const int64_t runs = std::max<int64_t>((p.seqlen + len - 1) / len, 1);
+    gr.work = (unsigned)(vecs * runs);
+    const dim3 grid((gr.work + kThreads - 1) / kThreads, 1, (unsigned)p.batch);
+    causal_conv_kernel<T, W, VEC><<<grid, kThreads, 0, stream>>>(p, gr);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t by_width(const ConvParams &p, hipStream_t stream) {
     switch (p.width) {
-        case 2: return run<T, 2, 1>(p, stream);
-        case 3: return run<T, 3, 1>(p, stream);
-        default: return run<T, 4, 1>(p, stream);
+        case 2: return run<T, 2>(p, stream);
+        case 3: return run<T, 3>(p, stream);
+        default: return run<T, 4>(p, stream);
     }
 }
 

@@ -145,7 +145,14 @@ struct VerifyParams {
     int64_t batch, vocab;
     int64_t t_bs, t_rs, d_bs, d_rs;
     int drafts;
+    // Segments of a row summed by the first of two launches (verify_segments);
+    // 1: one launch.
+    int segments;
+    int64_t segment;             // elements per segment
+    double *sums;                // [b,segments] in the workspace
 };
+// Chooses segments and segment from the sizes.
+void verify_segments(VerifyParams &p);
 hipError_t launch_verify_drafts(const VerifyParams &p, Elem e, hipStream_t stream);
 
 }  // namespace ssd

@@ -134,6 +134,23 @@ ssd_status check_verify(const ssd_verify_shape *s, ssd_dtype dtype) {
     return SSD_OK;
 }
 
+ssd::VerifyParams verify_params(const ssd_verify_shape *s) {
+    ssd::VerifyParams p = {};
+    p.batch = s->batch;
+    p.vocab = s->vocab;
+    p.t_bs = used_stride(s->batch, s->target_batch_stride);
+    p.t_rs = used_stride(s->drafts + 1, s->target_row_stride);
+    p.d_bs = used_stride(s->batch, s->draft_batch_stride);
+    p.d_rs = used_stride(s->drafts, s->draft_row_stride);
+    p.drafts = (int)s->drafts;
+    ssd::verify_segments(p);
+    return p;
+}
+
+size_t verify_workspace(const ssd::VerifyParams &p) {
+    return p.segments > 1 ? (size_t)p.batch * p.segments * sizeof(double) : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -335,7 +352,7 @@ ssd_status ssd_gated_norm_fwd(const void *x, const void *z, const float *weight,
 
 size_t ssd_verify_workspace_bytes(const ssd_verify_shape *shape, ssd_dtype dtype) {
     if (check_verify(shape, dtype) != SSD_OK) return 0;
-    return 0;
+    return verify_workspace(verify_params(shape));
 }
 
 ssd_status ssd_verify_drafts(const void *target_probs, const void *draft_probs, const int32_t *draft_tokens,
@@ -351,7 +368,8 @@ ssd_status ssd_verify_drafts(const void *target_probs, const void *draft_probs, 
     if (b > 0 && (!target_probs || !uniforms || !n_accepted || !next_token))
         return fail(SSD_ERR_NULL, "target_probs, uniforms, n_accepted and next_token are required");
     if (b > 0 && K > 0 && !draft_tokens) return fail(SSD_ERR_NULL, "draft_tokens is required");
-    const size_t ws_need = ssd_verify_workspace_bytes(s, dtype);
+    ssd::VerifyParams p = verify_params(s);
+    const size_t ws_need = verify_workspace(p);
     if (ws_need > 0 && !workspace) return fail(SSD_ERR_WORKSPACE, "workspace is NULL");
     if (workspace_bytes < ws_need)
         return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, ws_need);
@@ -370,7 +388,6 @@ ssd_status ssd_verify_drafts(const void *target_probs, const void *draft_probs, 
     if ((st = check_alias(o, in, allowed)) != SSD_OK) return st;
     if (b == 0) return SSD_OK;  // nothing to enqueue
 
-    ssd::VerifyParams p = {};
     p.target = target_probs;
     p.draft = K > 0 ? draft_probs : nullptr;
     p.tok = draft_tokens;
@@ -379,13 +396,7 @@ ssd_status ssd_verify_drafts(const void *target_probs, const void *draft_probs, 
     p.n_accepted = n_accepted;
     p.next_token = next_token;
     p.tokens = tokens;
-    p.batch = b;
-    p.vocab = V;
-    p.t_bs = used_stride(b, s->target_batch_stride);
-    p.t_rs = used_stride(K + 1, s->target_row_stride);
-    p.d_bs = used_stride(b, s->draft_batch_stride);
-    p.d_rs = used_stride(K, s->draft_row_stride);
-    p.drafts = (int)K;
+    p.sums = static_cast<double *>(workspace);
     (void)hipGetLastError();  // start from a clean error state
     return launched("verify_drafts", ssd::launch_verify_drafts(p, elem(dtype), static_cast<hipStream_t>(hip_stream)));
 }

@@ -1,115 +1,257 @@
 // Verification of drafted tokens: per sequence the first draft i with
 // u_i q_i(tok_i) >= p_i(tok_i), then a token from the residual
-// max(p_n - q_n, 0) (p_m when every draft is accepted) by inverse CDF.
+// r = max(p_n - q_n, 0) (p_m when every draft is accepted) by inverse CDF.
 //
 // Everything that decides is fp64: u q is exact there (24-bit factors), and
 // sums of fp32 values keep 29 spare bits, so that the order in which a row is
 // summed moves a border between two tokens by 1e-16 of the row's mass only.
-// One workgroup per sequence: each thread sums a contiguous piece of the row,
-// the pieces' prefix finds the piece that holds the cut, and its thread walks
-// it again.
+// The order is fixed, so equal inputs give equal tokens.
+//
+// Only the K tested probabilities and one row of p and q are needed.  A row is
+// summed in segments; the prefix over their sums finds the segment that holds
+// the cut, which is read again (from cache) with a few adjacent elements per
+// thread.  With many sequences a workgroup of 16 waves takes a whole row, its
+// waves' pieces being the segments; with few, a first launch sums the segments
+// of all rows on the whole GPU and a workgroup per row picks the token.
 #include "device_common.hpp"
 #include "kernels.hpp"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kSumThreads = 256;
+constexpr int kMaxSegments = 64;
 
 // A probability's mass: NaN and negative values count as none.
 __device__ __forceinline__ double mass(double v) { return v > 0.0 ? v : 0.0; }
 
+// What a sequence's drafts leave: the row to draw from.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void verify_drafts_kernel(VerifyParams p) {
-    __shared__ double piece[kThreads];
-    __shared__ int first_reject, found, last_mass;
-    const int64_t b = blockIdx.x;
-    const int tid = threadIdx.x, K = p.drafts;
-    const int64_t V = p.vocab;
-    const T *target = reinterpret_cast<const T *>(p.target) + b * p.t_bs;
-    const T *draft = p.draft ? reinterpret_cast<const T *>(p.draft) + b * p.d_bs : nullptr;
-    const int32_t *tok = K > 0 ? p.tok + b * K : nullptr;
-    const float *u = p.u + b * (K + 1);
-    int m = K;
-    if (p.lens) {
-        m = p.lens[b];
-        m = m < 0 ? 0 : (m > K ? K : m);
-    }
-    if (tid == 0) {
-        first_reject = m;
-        found = 0x7fffffff;
-        last_mass = -1;
-    }
-    __syncthreads();
-    for (int i = tid; i < m; i += kThreads) {
-        const int32_t v = tok[i];
-        bool ok = v >= 0 && v < V;
-        if (ok) {
-            const double q = draft ? (double)to_f32(draft[i * p.d_rs + v]) : 1.0;
-            ok = (double)u[i] * q < (double)to_f32(target[i * p.t_rs + v]);
-        }
-        if (!ok) atomicMin(&first_reject, i);
-    }
-    __syncthreads();
-    const int n = first_reject;
-    const T *pr = target + n * p.t_rs;
-    const T *qr = n < m && draft ? draft + n * p.d_rs : nullptr;
-    const int64_t zeroed = n < m && !draft ? (int64_t)tok[n] : -1;
-    const int64_t per = (V + kThreads - 1) / kThreads, lo = tid * per, hi = lo + per < V ? lo + per : V;
-    bool residual = n < m;
-    double total = 0.0, before = 0.0;
-    auto value = [&](int64_t v) {
-        const double pv = (double)to_f32(pr[v]);
-        if (!residual) return mass(pv);
-        if (qr) return mass(pv - (double)to_f32(qr[v]));
+struct Residual {
+    const T *p, *q;   // rows of the target and the draft (null without)
+    int64_t zeroed;   // token whose mass is taken away, or -1
+    bool drawn;       // a draft was rejected: r is the residual, not p itself
+
+    __device__ __forceinline__ double at(int64_t v) const {
+        const double pv = (double)to_f32(p[v]);
+        if (q) return mass(pv - (double)to_f32(q[v]));
         return v == zeroed ? 0.0 : mass(pv);
-    };
-    for (int pass = 0; pass < 2; ++pass) {
-        double sum = 0.0;
-        for (int64_t v = lo; v < hi; ++v) sum += value(v);
-        piece[tid] = sum;
-        __syncthreads();
-        total = 0.0;
-        for (int k = 0; k < kThreads; ++k) {
-            if (k == tid) before = total;
-            total += piece[k];
-        }
-        __syncthreads();
-        if (total > 0.0 || !residual) break;
-        residual = false;  // rounding left no mass: p_n itself
     }
-    const double cut = (double)u[K] * total;
-    double run = before;
-    int mine = -1;
-    for (int64_t v = lo; v < hi; ++v) {
-        const double r = value(v);
-        if (r > 0.0) mine = (int)v;
-        run += r;
-        if (run > cut) {
-            atomicMin(&found, (int)v);
-            break;
+    // Sum over [lo, hi) by the 64 lanes of a wave, each adding 16 bytes of
+    // elements at a time; the same in every lane.
+    __device__ __forceinline__ double wave_sum(int64_t lo, int64_t hi) const {
+        constexpr int VEC = 16 / sizeof(T);
+        const int lane = threadIdx.x & 63;
+        double s = 0.0;
+        int64_t v = lo + lane * VEC;
+        auto add = [&](const Pack<T, VEC> &pv, const Pack<T, VEC> &qv, int64_t from) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const double d = (double)to_f32(pv.v[i]);
+                s += q ? mass(d - (double)to_f32(qv.v[i])) : from + i == zeroed ? 0.0 : mass(d);
+            }
+        };
+        constexpr int STEP = 64 * VEC, U = 4;
+        for (; v + (U - 1) * STEP + VEC <= hi; v += U * STEP) {
+            Pack<T, VEC> pv[U], qv[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                pv[k] = *reinterpret_cast<const Pack<T, VEC> *>(p + v + k * STEP);
+                if (q) qv[k] = *reinterpret_cast<const Pack<T, VEC> *>(q + v + k * STEP);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) add(pv[k], qv[k], v + k * STEP);
         }
+        for (; v < hi; v += STEP) {
+            if (v + VEC <= hi) {
+                Pack<T, VEC> pv = *reinterpret_cast<const Pack<T, VEC> *>(p + v), qv = {};
+                if (q) qv = *reinterpret_cast<const Pack<T, VEC> *>(q + v);
+                add(pv, qv, v);
+            } else {
+                for (int64_t k = v; k < hi; ++k) s += at(k);
+            }
+        }
+        for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m);
+        return s;
     }
-    if (mine >= 0) atomicMax(&last_mass, mine);
+};
+
+__device__ __forceinline__ int drafts_of(const VerifyParams &p, int64_t b) {
+    const int m = p.lens ? p.lens[b] : p.drafts;
+    return m < 0 ? 0 : (m > p.drafts ? p.drafts : m);
+}
+
+// The number of accepted drafts of sequence b, by all threads of a workgroup;
+// *first is LDS.
+template <typename T>
+__device__ __forceinline__ int accepted_drafts(const VerifyParams &p, int64_t b, int m, int *first) {
+    if (threadIdx.x == 0) *first = m;
     __syncthreads();
-    // Rounding (or a uniform outside [0,1)) may leave no such token: the last
-    // one with mass, or V-1 for a row without any.
-    const int next = found != 0x7fffffff ? found : last_mass >= 0 ? last_mass : (int)(V - 1);
-    if (tid == 0) {
-        p.n_accepted[b] = n;
-        p.next_token[b] = next;
+    for (int i = threadIdx.x; i < m; i += blockDim.x) {
+        const int32_t v = p.tok[b * p.drafts + i];
+        bool ok = v >= 0 && v < p.vocab;
+        if (ok) {
+            const double q =
+                p.draft ? (double)to_f32(reinterpret_cast<const T *>(p.draft)[b * p.d_bs + i * p.d_rs + v]) : 1.0;
+            ok = (double)p.u[b * (p.drafts + 1) + i] * q <
+                 (double)to_f32(reinterpret_cast<const T *>(p.target)[b * p.t_bs + i * p.t_rs + v]);
+        }
+        if (!ok) atomicMin(first, i);
     }
+    __syncthreads();
+    return *first;
+}
+
+template <typename T>
+__device__ __forceinline__ Residual<T> residual_of(const VerifyParams &p, int64_t b, int n, int m) {
+    Residual<T> r;
+    r.p = reinterpret_cast<const T *>(p.target) + b * p.t_bs + n * p.t_rs;
+    r.drawn = n < m;
+    r.q = r.drawn && p.draft ? reinterpret_cast<const T *>(p.draft) + b * p.d_bs + n * p.d_rs : nullptr;
+    r.zeroed = r.drawn && !p.draft ? (int64_t)p.tok[b * p.drafts + n] : -1;
+    return r;
+}
+
+// First launch of a split call: n_accepted and the segments' sums.
+template <typename T>
+__global__ __launch_bounds__(kSumThreads) void verify_sums_kernel(VerifyParams p) {
+    __shared__ int first;
+    __shared__ double part[kSumThreads / 64];
+    const int64_t b = blockIdx.y;
+    const int m = drafts_of(p, b), n = accepted_drafts<T>(p, b, m, &first);
+    const Residual<T> r = residual_of<T>(p, b, n, m);
+    const int64_t lo = blockIdx.x * p.segment, hi = min(lo + p.segment, p.vocab);
+    constexpr int NW = kSumThreads / 64;
+    const int64_t per = (hi - lo + NW - 1) / NW;
+    const int w = threadIdx.x >> 6;
+    const double s = r.wave_sum(min(lo + w * per, hi), min(lo + (w + 1) * per, hi));
+    if ((threadIdx.x & 63) == 0) part[w] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double sum = 0.0;
+        for (int k = 0; k < NW; ++k) sum += part[k];
+        p.sums[b * p.segments + blockIdx.x] = sum;
+        if (blockIdx.x == 0) p.n_accepted[b] = n;
+    }
+}
+
+// The rest, one workgroup per sequence.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyParams p) {
+    __shared__ double sums[kMaxSegments], wave_sums[kWaves];
+    __shared__ int first, found, last_mass;
+    const int64_t b = blockIdx.x, V = p.vocab;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, K = p.drafts;
+    const int m = drafts_of(p, b);
+    int n;
+    if (p.segments > 1) {
+        n = p.n_accepted[b];
+    } else {
+        n = accepted_drafts<T>(p, b, m, &first);
+        if (tid == 0) p.n_accepted[b] = n;
+    }
+    Residual<T> r = residual_of<T>(p, b, n, m);
+    int segments = p.segments;
+    int64_t segment = p.segment;
+    if (segments > 1) {
+        if (tid < segments) sums[tid] = p.sums[b * segments + tid];
+        __syncthreads();
+    }
+    double total = 0.0;
+    for (int pass = 0; pass < 2; ++pass) {
+        if (p.segments == 1 || pass == 1) {
+            segments = kWaves;
+            segment = (V + kWaves - 1) / kWaves;
+            const double s = r.wave_sum(min(wave * segment, V), min((wave + 1) * segment, V));
+            if (lane == 0) sums[wave] = s;
+            __syncthreads();
+        }
+        total = 0.0;
+        for (int k = 0; k < segments; ++k) total += sums[k];
+        if (total > 0.0 || !r.drawn) break;
+        // Rounding left the residual without mass: p_n takes its place.
+        r.drawn = false;
+        r.q = nullptr;
+        r.zeroed = -1;
+        __syncthreads();
+    }
+    const double cut = (double)p.u[b * (K + 1) + K] * total;
+    // The segment with the cut: the first whose end passes it, or the last
+    // with mass (a uniform outside [0,1), rounding).
+    int seg = -1;
+    double before = 0.0, run = 0.0;
+    for (int k = 0; k < segments; ++k) {
+        const double end = run + sums[k];
+        if (sums[k] > 0.0) {
+            seg = k;
+            before = run;
+            if (end > cut) break;
+        }
+        run = end;
+    }
+    int next = (int)(V - 1);  // a row without mass
+    if (seg >= 0) {
+        if (tid == 0) {
+            found = 0x7fffffff;
+            last_mass = -1;
+        }
+        const int64_t lo = seg * segment, hi = min(lo + segment, V), per = (hi - lo + kThreads - 1) / kThreads;
+        const int64_t a = min(lo + tid * per, hi), e = min(a + per, hi);
+        double s = 0.0;
+        for (int64_t v = a; v < e; ++v) s += r.at(v);
+        double pre = s;  // inclusive prefix over the wave's lanes
+        for (int k = 1; k < 64; k <<= 1) {
+            const double o = __shfl_up(pre, k);
+            if (lane >= k) pre += o;
+        }
+        if (lane == 63) wave_sums[wave] = pre;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) before += wave_sums[w];
+        if (s > 0.0) {
+            // This thread's elements, from the sum before them.
+            double at = before + (pre - s);
+            int last = -1;
+            for (int64_t v = a; v < e; ++v) {
+                const double x = r.at(v);
+                if (x > 0.0) last = (int)v;
+                at += x;
+                if (x > 0.0 && at > cut) {
+                    atomicMin(&found, (int)v);
+                    break;
+                }
+            }
+            atomicMax(&last_mass, last);
+        }
+        __syncthreads();
+        next = found != 0x7fffffff ? found : last_mass;
+    }
+    if (tid == 0) p.next_token[b] = next;
     if (p.tokens)
-        for (int i = tid; i <= K; i += kThreads) p.tokens[b * (K + 1) + i] = i < n ? tok[i] : i == n ? next : -1;
+        for (int i = tid; i <= K; i += kThreads)
+            p.tokens[b * (K + 1) + i] = i < n ? p.tok[b * K + i] : i == n ? next : -1;
 }
 
 template <typename T>
 hipError_t run(const VerifyParams &p, hipStream_t stream) {
-    verify_drafts_kernel<T><<<(unsigned)p.batch, kThreads, 0, stream>>>(p);
+    if (p.segments > 1) {
+        verify_sums_kernel<T><<<dim3(p.segments, (unsigned)p.batch), kSumThreads, 0, stream>>>(p);
+        const hipError_t r = hipGetLastError();
+        if (r != hipSuccess) return r;
+    }
+    verify_pick_kernel<T><<<(unsigned)p.batch, kThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 }  // namespace
+
+void verify_segments(VerifyParams &p) {
+    // Split while the rows alone leave compute units idle and a segment keeps
+    // at least 4096 elements (16 per thread of its workgroup).
+    const int64_t want = std::min<int64_t>({kMaxSegments, 256 / std::max<int64_t>(p.batch, 1), p.vocab / 4096});
+    p.segments = want >= 4 ? (int)want : 1;
+    p.segment = (p.vocab + p.segments - 1) / p.segments;
+}
 
 hipError_t launch_verify_drafts(const VerifyParams &p, Elem e, hipStream_t stream) {
     return e == Elem::BF16 ? run<bf16>(p, stream) : run<float>(p, stream);
