@@ -369,40 +369,54 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _dense(name, t, shape, dtype, device):
+    """_expect at the cost of one condition for a tensor that fits (single
+    tokens are bound by the time of the call itself)."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _expect(name, t, shape, dtype, device)
+
+
 def _strided(name, t, shape, dtype, device, inner=1):
     """Checks a tensor argument whose leading dimensions may be strided and
     whose last `inner` dimensions are contiguous; returns its strides."""
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     st = t.stride()
+    if st[-1] == 1 and (inner == 1 or st[-2] == shape[-1]):
+        return st
     want = 1
     for k in range(1, inner + 1):
-        if st[-k] != want and t.shape[-k] > 1 and t.numel() > 0:
+        if st[-k] != want and shape[-k] > 1 and t.numel() > 0:
             raise ValueError(f"{name} must be contiguous in its last {inner} dimension(s)" if inner > 1
                              else f"{name} must be contiguous in its last dimension")
-        want *= t.shape[-k]
+        want *= shape[-k]
     return st
 
 
+def _elsewhere(torch, t, stream):
+    """Whether a call on tensor t has to leave the current device or stream."""
+    return t.is_cuda and (stream is not None or t.device.index != torch.cuda.current_device())
+
+
 def _scope(torch, t, stream):
-    """What a call on tensor t has to run inside: t's device and, where one is
-    given, `stream` (a raw handle), so that tensors made by the call belong to
-    the stream that uses them; None where both are current already."""
-    if not t.is_cuda:
-        raise ValueError(f"tensors must be on a GPU device, got {t.device}")
+    """What such a call runs inside: t's device and, where one is given,
+    `stream` (a raw handle), so that tensors made by the call belong to the
+    stream that uses them."""
     if stream is None:
-        return None if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+        return torch.cuda.device(t.device)
     if stream == 0:
         return torch.cuda.stream(torch.cuda.default_stream(t.device))
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device))
 
 
 def _raw_stream(torch, device):
-    return torch.cuda.current_stream(device).cuda_stream or None
+    """The current stream's handle, without making a stream object of it
+    (torch.cuda.current_stream takes 2 us, a fifth of a single token's call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) or None
 
 
 def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, state_out_idx=None, *, split=None, activation="silu",
@@ -424,9 +438,8 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, state_out_idx=Non
 
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("x must be [b,T,Ch] and weight [Ch,W]")
-    scope = _scope(torch, x, stream) if x.is_cuda else None
-    if scope is not None:
-        with scope:
+    if _elsewhere(torch, x, stream):
+        with _scope(torch, x, stream):
             return ssd_causal_conv_fwd(x, weight, bias, init_state, state_out_idx, split=split, activation=activation,
                                        out=out, final_state=final_state, return_final_state=return_final_state,
                                        state_out=state_out)
@@ -434,7 +447,7 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, state_out_idx=Non
     w = weight.shape[1]
     code, dtype, dev = _dtype_code(torch, x), x.dtype, x.device
     st = _strided("x", x, x.shape, dtype, dev)
-    _expect("weight", weight, (ch, w), torch.float32, dev)
+    _dense("weight", weight, (ch, w), torch.float32, dev)
     if activation not in (None, "silu"):
         raise ValueError(f"activation must be 'silu' or None, got {activation!r}")
     sizes = [ch] if split is None else [int(k) for k in split]
@@ -442,11 +455,11 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, state_out_idx=Non
         raise ValueError(f"split must be one to three positive sizes adding up to {ch}, got {split}")
     held = (b, w - 1, ch)
     if bias is not None:
-        _expect("bias", bias, (ch,), torch.float32, dev)
+        _dense("bias", bias, (ch,), torch.float32, dev)
     if init_state is not None:
-        _expect("init_state", init_state, held, dtype, dev)
+        _dense("init_state", init_state, held, dtype, dev)
     if state_out_idx is not None:
-        _expect("state_out_idx", state_out_idx, (b,), torch.int32, dev)
+        _dense("state_out_idx", state_out_idx, (b,), torch.int32, dev)
     elif state_out is not None:
         raise ValueError("state_out needs state_out_idx")
     if out is None:
@@ -456,20 +469,20 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, state_out_idx=Non
         if len(outs) != len(sizes):
             raise ValueError(f"out must hold {len(sizes)} tensors, got {len(outs)}")
         for k, (o, n) in enumerate(zip(outs, sizes)):
-            _expect("out" if split is None else f"out[{k}]", o, (b, T, n), dtype, dev)
+            _dense("out" if split is None else f"out[{k}]", o, (b, T, n), dtype, dev)
     if final_state is not None:
-        _expect("final_state", final_state, held, dtype, dev)
+        _dense("final_state", final_state, held, dtype, dev)
     if state_out is not None:
-        _expect("state_out", state_out, held, dtype, dev)
+        _dense("state_out", state_out, held, dtype, dev)
     if not x.is_cuda:
         raise ValueError(f"tensors must be on a GPU device, x is on {dev}")
     lib = _load()
     if outs is None:
-        outs = [torch.empty((b, T, n), dtype=dtype, device=dev) for n in sizes]
+        outs = [x.new_empty((b, T, n)) for n in sizes]
     if final_state is None and return_final_state:
-        final_state = torch.empty(held, dtype=dtype, device=dev)
+        final_state = x.new_empty(held)
     if state_out is None and state_out_idx is not None:
-        state_out = torch.empty(held, dtype=dtype, device=dev)
+        state_out = x.new_empty(held)
     pad = [0] * (3 - len(sizes))
     shape = ssd_conv_shape(b, T, (ctypes.c_int64 * 3)(*sizes, *pad), w, st[0], st[1])
     _check(lib.ssd_causal_conv_fwd(_addr(x), _addr(weight), _addr(bias), _addr(init_state),
@@ -501,9 +514,8 @@ def ssd_selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, i
 
     if u.dim() != 3 or A.dim() != 2 or B.dim() != 4:
         raise ValueError("u must be [b,T,Dm], A [Dm,N] and B, C [b,T,G,N]")
-    scope = _scope(torch, u, stream) if u.is_cuda else None
-    if scope is not None:
-        with scope:
+    if _elsewhere(torch, u, stream):
+        with _scope(torch, u, stream):
             return ssd_selective_scan_fwd(u, delta, A, B, C, D, z, delta_bias, init_state, state_out_idx,
                                           delta_softplus=delta_softplus, y=y, final_state=final_state,
                                           return_final_state=return_final_state, state_out=state_out,
@@ -517,26 +529,26 @@ def ssd_selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, i
     sz = _strided("z", z, u.shape, dtype, dev) if z is not None else (0, 0)
     sb = _strided("B", B, (b, T, G, N), dtype, dev, 2)
     sc = _strided("C", C, (b, T, G, N), dtype, dev, 2)
-    _expect("A", A, (ch, N), f32, dev)
+    _dense("A", A, (ch, N), f32, dev)
     if D is not None:
-        _expect("D", D, (ch,), f32, dev)
+        _dense("D", D, (ch,), f32, dev)
     if delta_bias is not None:
-        _expect("delta_bias", delta_bias, (ch,), f32, dev)
+        _dense("delta_bias", delta_bias, (ch,), f32, dev)
     state = (b, ch, N)
     if init_state is not None:
-        _expect("init_state", init_state, state, f32, dev)
+        _dense("init_state", init_state, state, f32, dev)
     if state_out_idx is not None:
-        _expect("state_out_idx", state_out_idx, (b,), torch.int32, dev)
+        _dense("state_out_idx", state_out_idx, (b,), torch.int32, dev)
     elif state_out is not None:
         raise ValueError("state_out needs state_out_idx")
     if y is not None:
-        _expect("y", y, u.shape, dtype, dev)
+        _dense("y", y, u.shape, dtype, dev)
     if final_state is not None:
-        _expect("final_state", final_state, state, f32, dev)
+        _dense("final_state", final_state, state, f32, dev)
     if state_out is not None:
-        _expect("state_out", state_out, state, f32, dev)
+        _dense("state_out", state_out, state, f32, dev)
     if workspace is not None:
-        _expect("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+        _dense("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
     if not u.is_cuda:
         raise ValueError(f"tensors must be on a GPU device, u is on {dev}")
     lib = _load()
@@ -550,11 +562,11 @@ def ssd_selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, i
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     if y is None:
-        y = torch.empty((b, T, ch), dtype=dtype, device=dev)
+        y = u.new_empty((b, T, ch))
     if final_state is None and return_final_state:
-        final_state = torch.empty(state, dtype=f32, device=dev)
+        final_state = A.new_empty(state)
     if state_out is None and state_out_idx is not None:
-        state_out = torch.empty(state, dtype=f32, device=dev)
+        state_out = A.new_empty(state)
     _check(lib.ssd_selective_scan_fwd(_addr(u), _addr(delta), _addr(A), _addr(B), _addr(C), _addr(D), _addr(z),
                                       _addr(delta_bias), 1 if delta_softplus else 0, _addr(init_state), _addr(y),
                                       _addr(final_state), _addr(state_out_idx), _addr(state_out), ref, code,
@@ -589,9 +601,8 @@ def ssd_gated_norm_fwd(x, z=None, weight=None, *, ngroups: int = 1, eps: float =
 
     if x.dim() < 1:
         raise ValueError("x must be [..., dim]")
-    scope = _scope(torch, x, stream) if x.is_cuda else None
-    if scope is not None:
-        with scope:
+    if _elsewhere(torch, x, stream):
+        with _scope(torch, x, stream):
             return ssd_gated_norm_fwd(x, z, weight, ngroups=ngroups, eps=eps, norm_before_gate=norm_before_gate,
                                       out=out)
     code, dtype, dev = _dtype_code(torch, x), x.dtype, x.device
@@ -600,14 +611,14 @@ def ssd_gated_norm_fwd(x, z=None, weight=None, *, ngroups: int = 1, eps: float =
     if z is not None:
         _strided("z", z, x.shape, dtype, dev)
     if weight is not None:
-        _expect("weight", weight, (dim,), torch.float32, dev)
+        _dense("weight", weight, (dim,), torch.float32, dev)
     if out is not None:
-        _expect("out", out, x.shape, dtype, dev)
+        _dense("out", out, x.shape, dtype, dev)
     if not x.is_cuda:
         raise ValueError(f"tensors must be on a GPU device, x is on {dev}")
     lib = _load()
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=dev)
+        out = x.new_empty(x.shape)
     T = x.shape[-2] if x.dim() > 1 else 1
     b = x.numel() // (T * dim) if T * dim else 0
     sx = _two_levels("x", x, b, T)
@@ -640,9 +651,8 @@ def ssd_verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, dr
 
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:
         raise ValueError("target_probs must be [b,K+1,V]")
-    scope = _scope(torch, target_probs, stream) if target_probs.is_cuda else None
-    if scope is not None:
-        with scope:
+    if _elsewhere(torch, target_probs, stream):
+        with _scope(torch, target_probs, stream):
             return ssd_verify_drafts(target_probs, draft_tokens, uniforms, draft_probs, draft_lens,
                                      n_accepted=n_accepted, next_token=next_token, tokens=tokens,
                                      workspace=workspace)
@@ -652,18 +662,18 @@ def ssd_verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, dr
     code, dtype, dev = _dtype_code(torch, target_probs, "target_probs"), target_probs.dtype, target_probs.device
     st = _strided("target_probs", target_probs, target_probs.shape, dtype, dev)
     sd = _strided("draft_probs", draft_probs, (b, K, V), dtype, dev) if draft_probs is not None else (0, 0)
-    _expect("draft_tokens", draft_tokens, (b, K), i32, dev)
-    _expect("uniforms", uniforms, (b, rows), torch.float32, dev)
+    _dense("draft_tokens", draft_tokens, (b, K), i32, dev)
+    _dense("uniforms", uniforms, (b, rows), torch.float32, dev)
     if draft_lens is not None:
-        _expect("draft_lens", draft_lens, (b,), i32, dev)
+        _dense("draft_lens", draft_lens, (b,), i32, dev)
     if n_accepted is not None:
-        _expect("n_accepted", n_accepted, (b,), i32, dev)
+        _dense("n_accepted", n_accepted, (b,), i32, dev)
     if next_token is not None:
-        _expect("next_token", next_token, (b,), i32, dev)
+        _dense("next_token", next_token, (b,), i32, dev)
     if tokens is not None:
-        _expect("tokens", tokens, (b, rows), i32, dev)
+        _dense("tokens", tokens, (b, rows), i32, dev)
     if workspace is not None:
-        _expect("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+        _dense("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
     if not target_probs.is_cuda:
         raise ValueError(f"tensors must be on a GPU device, target_probs is on {dev}")
     lib = _load()
@@ -676,11 +686,11 @@ def ssd_verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, dr
         if ws_bytes > 0:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
     if n_accepted is None:
-        n_accepted = torch.empty(b, dtype=i32, device=dev)
+        n_accepted = draft_tokens.new_empty(b)
     if next_token is None:
-        next_token = torch.empty(b, dtype=i32, device=dev)
+        next_token = draft_tokens.new_empty(b)
     if tokens is None:
-        tokens = torch.empty((b, rows), dtype=i32, device=dev)
+        tokens = draft_tokens.new_empty((b, rows))
     _check(lib.ssd_verify_drafts(_addr(target_probs), _addr(draft_probs), _addr(draft_tokens), _addr(draft_lens),
                                  _addr(uniforms), _addr(n_accepted), _addr(next_token), _addr(tokens), ref, code,
                                  _addr(workspace), ws_bytes, _raw_stream(torch, dev)))

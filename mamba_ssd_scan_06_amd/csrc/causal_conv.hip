@@ -26,33 +26,129 @@ struct ConvGrid {
     int run;          // tokens per run
 };
 
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load_pack(const T *p, int valid) {
-    if (valid == VEC) return *reinterpret_cast<const Pack<T, VEC> *>(p);
-    Pack<T, VEC> r;
+// One thread's run: channels c0 .. c0 + valid - 1 of x, from channel co of an
+// output with `width` channels.  WHOLE: all VEC of them.
+template <typename T, int W, bool WHOLE>
+__device__ __forceinline__ void conv_run(const ConvParams &p, unsigned run, int run_len, int c0, int valid, T *out,
+                                         int width) {
+    constexpr int VEC = 16 / sizeof(T);
+    const int64_t b = blockIdx.z, T_len = p.seqlen;
+    const T *x = reinterpret_cast<const T *>(p.x) + b * p.x_bs + c0;
+    const int64_t held = (b * (W - 1)) * p.total + c0;
+    const int64_t t0 = (int64_t)run * run_len, t1 = min(t0 + run_len, T_len);
+    auto load = [&](const auto *from) {
+        if constexpr (WHOLE) return load_words(from);
+        else return load_first(from, valid);
+    };
+    auto store = [&](T *to, const u32x4 &v) {
+        if constexpr (WHOLE) store_words(to, v);
+        else store_first(to, v, valid);
+    };
+
+    // All of a thread's loads before its first store: the weights, the W-1
+    // inputs before the run (hist[k] is token t0 - (W-1) + k) and the states'
+    // rows.  A single token is bound by the latency of this one round.
+    float w[W][VEC], bias[VEC];
+    if constexpr (WHOLE) {
+        constexpr int WV = VEC * W / 4;
+        u32x4 wv[WV];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) r.v[i] = i < valid ? p[i] : from_f32<T>(0.0f);
-    return r;
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_pack(T *p, const Pack<T, VEC> &v, int valid) {
-    if (valid == VEC) {
-        *reinterpret_cast<Pack<T, VEC> *>(p) = v;
-        return;
+        for (int k = 0; k < WV; ++k) wv[k] = load_words(p.weight + (int64_t)c0 * W + 4 * k);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][i] = word_f32(wv[(i * W + k) / 4], (i * W + k) % 4, float());
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][i] = p.weight[(int64_t)(c0 + min(i, valid - 1)) * W + k];
     }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        if (i < valid) p[i] = v.v[i];
+    for (int i = 0; i < VEC; ++i) bias[i] = p.bias ? p.bias[c0 + (WHOLE ? i : min(i, valid - 1))] : 0.0f;
+    u32x4 hist[W - 1];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) hist[k] = u32x4{0u, 0u, 0u, 0u};
+    if (run > 0) {  // t0 >= run_len >= W - 1
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) hist[k] = load(x + (t0 - (W - 1) + k) * p.x_ts);
+    } else if (p.init_state) {
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k)
+            hist[k] = load(reinterpret_cast<const T *>(p.init_state) + held + (int64_t)k * p.total);
+    }
+    // Both states come from run 0's threads, which have read init_state by
+    // the time they store: final_state may be the same memory.
+    if (run == 0 && (p.state_out || p.final_state)) {
+        u32x4 at[W - 1], fin[W - 1];
+        auto inputs = [&](u32x4 (&v)[W - 1], int64_t last) {  // the W-1 inputs ending at token `last`
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) {
+                const int64_t t = last - (W - 2) + k;  // >= -(W-1); a uniform condition
+                if (t >= 0) {
+                    v[k] = load(x + t * p.x_ts);
+                } else {
+                    v[k] = hist[0];
+#pragma unroll
+                    for (int m = 1; m < W - 1; ++m)
+                        if (t + (W - 1) == m) v[k] = hist[m];
+                }
+            }
+        };
+        auto keep = [&](void *to, const u32x4 (&v)[W - 1]) {
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) store(reinterpret_cast<T *>(to) + held + (int64_t)k * p.total, v[k]);
+        };
+        if (p.state_out) {
+            const int64_t j = p.state_out_idx[b];
+            inputs(at, j < -1 ? -1 : (j > T_len - 1 ? T_len - 1 : j));
+        }
+        if (p.final_state) inputs(fin, T_len - 1);
+        if (p.state_out) keep(p.state_out, at);
+        if (p.final_state) keep(p.final_state, fin);
+    }
+
+    // last[k]: the inputs of tokens t - (W-1) + k in fp32.
+    float last[W - 1][VEC];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) last[k][i] = word_f32(hist[k], i, T());
+    auto token = [&](const u32x4 &v) {
+        float r[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const float cur = word_f32(v, i, T());
+            float acc = bias[i];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], last[k][i], acc);
+            acc = fmaf(w[W - 1][i], cur, acc);
+#pragma unroll
+            for (int k = 0; k + 1 < W - 1; ++k) last[k][i] = last[k + 1][i];
+            last[W - 2][i] = cur;
+            r[i] = p.silu ? silu(acc) : acc;
+        }
+        return to_words(r, T());
+    };
+    out += b * T_len * width;
+    int64_t t = t0;
+    for (; t + kBatchLoads <= t1; t += kBatchLoads) {
+        u32x4 v[kBatchLoads];
+#pragma unroll
+        for (int q = 0; q < kBatchLoads; ++q) v[q] = load(x + (t + q) * p.x_ts);
+#pragma unroll
+        for (int q = 0; q < kBatchLoads; ++q) store(out + (t + q) * width, token(v[q]));
+    }
+    for (; t < t1; ++t) store(out + t * width, token(load(x + t * p.x_ts)));
 }
 
-template <typename T, int W, int VEC>
+template <typename T, int W>
 __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvParams p, ConvGrid gr) {
-    using P = Pack<T, VEC>;
+    constexpr int VEC = 16 / sizeof(T);
     const unsigned id = blockIdx.x * kThreads + threadIdx.x;
     if (id >= gr.work) return;
     const unsigned run = id / gr.vecs_all;
     int cv = (int)(id - run * gr.vecs_all);
-    const int64_t b = blockIdx.z, T_len = p.seqlen;
     // The output this vector of channels belongs to, its first channel there
     // (co) and overall (c0).
     int o = 0, base = 0;
@@ -67,104 +163,10 @@ __global__ __launch_bounds__(kThreads) void causal_conv_kernel(ConvParams p, Con
         }
     }
     const int width = o == 0 ? p.channels[0] : o == 1 ? p.channels[1] : p.channels[2];
-    const int co = cv * VEC, c0 = base + co, valid = min(VEC, width - co);
-    const T *x = reinterpret_cast<const T *>(p.x) + b * p.x_bs + c0;
-    T *out = reinterpret_cast<T *>(o == 0 ? p.out[0] : o == 1 ? p.out[1] : p.out[2]) + b * T_len * width + co;
-    const int64_t held = (b * (W - 1)) * p.total + c0;
-    const int64_t t0 = (int64_t)run * gr.run, t1 = min(t0 + gr.run, T_len);
-
-    // The W-1 inputs before the run: hist[k] is token t0 - (W-1) + k.
-    P hist[W - 1];
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        const int64_t t = t0 - (W - 1) + k;
-        if (t >= 0) {
-            hist[k] = load_pack<T, VEC>(x + t * p.x_ts, valid);
-        } else if (p.init_state) {  // t >= -(W-1): run 0
-            hist[k] = load_pack<T, VEC>(reinterpret_cast<const T *>(p.init_state) + held + (W - 1 + t) * p.total, valid);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) hist[k].v[i] = from_f32<T>(0.0f);
-        }
-    }
-    // Both states come from run 0's threads, which have read init_state by
-    // now: final_state may be the same memory.
-    if (run == 0 && (p.state_out || p.final_state)) {
-        auto keep = [&](void *to, int64_t last) {  // the W-1 inputs ending at token `last`
-            P v[W - 1];
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) {
-                const int64_t t = last - (W - 2) + k;  // >= -(W-1)
-                if (t >= 0) {
-                    v[k] = load_pack<T, VEC>(x + t * p.x_ts, valid);
-                } else {
-                    v[k] = hist[0];
-#pragma unroll
-                    for (int m = 1; m < W - 1; ++m)
-                        if (t + (W - 1) == m) v[k] = hist[m];
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k)
-                store_pack<T, VEC>(reinterpret_cast<T *>(to) + held + (int64_t)k * p.total, v[k], valid);
-        };
-        if (p.state_out) {
-            const int64_t j = p.state_out_idx[b];
-            keep(p.state_out, j < -1 ? -1 : (j > T_len - 1 ? T_len - 1 : j));
-        }
-        if (p.final_state) keep(p.final_state, T_len - 1);
-    }
-    if (t0 >= t1) return;
-
-    float w[W][VEC], bias[VEC];
-    if (valid == VEC) {
-        const Pack<float, VEC * W> wv = *reinterpret_cast<const Pack<float, VEC * W> *>(p.weight + (int64_t)c0 * W);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-#pragma unroll
-            for (int k = 0; k < W; ++k) w[k][i] = wv.v[i * W + k];
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-#pragma unroll
-            for (int k = 0; k < W; ++k) w[k][i] = i < valid ? p.weight[(int64_t)(c0 + i) * W + k] : 0.0f;
-    }
-    const Pack<float, VEC> bv = p.bias ? load_pack<float, VEC>(p.bias + c0, valid) : Pack<float, VEC>{};
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) bias[i] = bv.v[i];
-
-    // last[k]: the inputs of tokens t - (W-1) + k in fp32.
-    float last[W - 1][VEC];
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) last[k][i] = to_f32(hist[k].v[i]);
-    auto token = [&](const P &v) {
-        P r;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float cur = to_f32(v.v[i]);
-            float acc = bias[i];
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) acc = fmaf(w[k][i], last[k][i], acc);
-            acc = fmaf(w[W - 1][i], cur, acc);
-#pragma unroll
-            for (int k = 0; k + 1 < W - 1; ++k) last[k][i] = last[k + 1][i];
-            last[W - 2][i] = cur;
-            r.v[i] = from_f32<T>(p.silu ? silu(acc) : acc);
-        }
-        return r;
-    };
-    int64_t t = t0;
-    if (valid == VEC)
-        for (; t + kBatchLoads <= t1; t += kBatchLoads) {
-            P v[kBatchLoads];
-#pragma unroll
-            for (int q = 0; q < kBatchLoads; ++q) v[q] = *reinterpret_cast<const P *>(x + (t + q) * p.x_ts);
-#pragma unroll
-            for (int q = 0; q < kBatchLoads; ++q) *reinterpret_cast<P *>(out + (t + q) * width) = token(v[q]);
-        }
-    for (; t < t1; ++t) store_pack<T, VEC>(out + t * width, token(load_pack<T, VEC>(x + t * p.x_ts, valid)), valid);
+    const int co = cv * VEC, valid = min(VEC, width - co);
+    T *out = reinterpret_cast<T *>(o == 0 ? p.out[0] : o == 1 ? p.out[1] : p.out[2]) + co;
+    if (valid == VEC) conv_run<T, W, true>(p, run, gr.run, base + co, valid, out, width);
+    else conv_run<T, W, false>(p, run, gr.run, base + co, valid, out, width);
 }
 
 template <typename T, int W>
@@ -187,7 +189,7 @@ hipError_t run(const ConvParams &p, hipStream_t stream) {
     const int64_t runs = std::max<int64_t>((p.seqlen + len - 1) / len, 1);
     gr.work = (unsigned)(vecs * runs);
     const dim3 grid((gr.work + kThreads - 1) / kThreads, 1, (unsigned)p.batch);
-    causal_conv_kernel<T, W, VEC><<<grid, kThreads, 0, stream>>>(p, gr);
+    causal_conv_kernel<T, W><<<grid, kThreads, 0, stream>>>(p, gr);
     return hipGetLastError();
 }
 

@@ -280,6 +280,68 @@ struct __attribute__((packed, aligned(sizeof(T)))) Pack {
     T v[N];
 };
 
+// The same as raw 32-bit words, for loads that stay in flight: a Pack of bf16
+// is taken apart right after its load (which waits for it), words only where
+// they are used.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_at2 __attribute__((aligned(2), may_alias));
+typedef u32x4 u32x4_at4 __attribute__((aligned(4), may_alias));
+template <typename T>
+__device__ __forceinline__ u32x4 load_words(const T *p) {
+    if constexpr (sizeof(T) == 2) return *reinterpret_cast<const u32x4_at2 *>(p);
+    else return *reinterpret_cast<const u32x4_at4 *>(p);
+}
+template <typename T>
+__device__ __forceinline__ void store_words(T *p, const u32x4 &v) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<u32x4_at2 *>(p) = v;
+    else *reinterpret_cast<u32x4_at4 *>(p) = v;
+}
+// The first `valid` (1 or more) elements at p, the last of them repeated after;
+// nothing beyond them is read.  No branches: where a call may be whole or
+// partial, each takes code of its own instead of meeting in one register.
+template <typename T>
+__device__ __forceinline__ u32x4 load_first(const T *p, int valid) {
+    constexpr int VEC = 16 / sizeof(T);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const T e = p[min(i, valid - 1)];
+        if constexpr (sizeof(T) == 2) w[i >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, e) << (16 * (i & 1));
+        else w[i] = __builtin_bit_cast(uint32_t, e);
+    }
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+// Element i of such words in fp32.
+__device__ __forceinline__ float word_f32(const u32x4 &v, int i, bf16) {
+    return __builtin_bit_cast(float, i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16);
+}
+__device__ __forceinline__ float word_f32(const u32x4 &v, int i, float) {
+    const uint32_t w = v[i];  // a value: bit_cast of a vector's element takes the vector's first
+    return __builtin_bit_cast(float, w);
+}
+// Stores the first `valid` elements.
+template <typename T>
+__device__ __forceinline__ void store_first(T *p, const u32x4 &v, int valid) {
+    constexpr int VEC = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        if (i < valid) {
+            if constexpr (sizeof(T) == 2) p[i] = __builtin_bit_cast(T, (uint16_t)(v[i >> 1] >> (16 * (i & 1))));
+            else p[i] = word_f32(v, i, T());
+        }
+}
+// fp32 values rounded into such words.
+__device__ __forceinline__ u32x4 to_words(const float (&f)[8], bf16) {
+    bf16x8 v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (bf16)f[i];
+    return __builtin_bit_cast(u32x4, v);
+}
+__device__ __forceinline__ u32x4 to_words(const float (&f)[4], float) {
+    return u32x4{__builtin_bit_cast(uint32_t, f[0]), __builtin_bit_cast(uint32_t, f[1]),
+                 __builtin_bit_cast(uint32_t, f[2]), __builtin_bit_cast(uint32_t, f[3])};
+}
+
 // Calls f(std::integral_constant<int, I>{}) for I = 0 .. N-1 (unrolled, with
 // compile-time indices, e.g. for register arrays).
 template <typename F, int... I>

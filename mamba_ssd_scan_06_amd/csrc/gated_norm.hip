@@ -20,15 +20,6 @@ struct NormGrid {
     int lanes;
 };
 
-template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> load_piece(const T *p, int valid) {
-    if (valid >= VEC) return *reinterpret_cast<const Pack<T, VEC> *>(p);
-    Pack<T, VEC> r;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) r.v[i] = i < valid ? p[i] : from_f32<T>(0.0f);
-    return r;
-}
-
 // Sum over a part's lanes (all of the workgroup where lanes > 64).
 __device__ __forceinline__ float part_sum(float v, int lanes, float *waves) {
     for (int m = 1; m < (lanes < 64 ? lanes : 64); m <<= 1) v += __shfl_xor(v, m);
@@ -43,7 +34,8 @@ __device__ __forceinline__ float part_sum(float v, int lanes, float *waves) {
     return v;
 }
 
-// HELD: pieces per thread; 0: any number, read twice.  MAX: threads at most.
+// HELD: pieces per thread; 0: any number (or a part shorter than a piece),
+// read twice.  MAX: threads at most.
 template <typename T, int HELD, int MAX>
 __global__ __launch_bounds__(MAX) void gated_norm_kernel(NormParams p, NormGrid gr) {
     constexpr int VEC = 16 / sizeof(T);
@@ -63,73 +55,98 @@ __global__ __launch_bounds__(MAX) void gated_norm_kernel(NormParams p, NormGrid 
         T *out = reinterpret_cast<T *>(p.out) + (int64_t)row * p.dim + c0;
         const float *weight = p.weight ? p.weight + c0 : nullptr;
 
-        auto finish = [&](const float (&v)[VEC], const Pack<T, VEC> &zr, float scale, int c) {
-            const int valid = p.group_dim - c;
-            const Pack<float, VEC> wv = weight ? load_piece<float, VEC>(weight + c, valid) : Pack<float, VEC>{};
-            Pack<T, VEC> o;
+        // The values to normalise; they include the gate where it comes first.
+        auto values = [&](const u32x4 &xr, const u32x4 &zr, float (&v)[VEC]) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                v[i] = word_f32(xr, i, T());
+                if (z && !p.norm_before_gate) v[i] *= silu(word_f32(zr, i, T()));
+            }
+        };
+        auto scaled = [&](const float (&v)[VEC], const u32x4 &zr, const u32x4 (&wv)[VEC / 4], float scale) {
+            float o[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 float f = v[i] * scale;
-                if (weight) f *= wv.v[i];
-                if (z && p.norm_before_gate) f *= silu(to_f32(zr.v[i]));
-                o.v[i] = from_f32<T>(f);
+                if (weight) f *= word_f32(wv[i / 4], i % 4, float());
+                if (z && p.norm_before_gate) f *= silu(word_f32(zr, i, T()));
+                o[i] = f;
             }
-            if (mine >= parts) return;
-            if (valid >= VEC) {
-                *reinterpret_cast<Pack<T, VEC> *>(out + c) = o;
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (i < valid) out[c + i] = o.v[i];
-            }
+            return to_words(o, T());
         };
-        // The values to normalise; they include the gate where it comes first.
-        auto values = [&](const Pack<T, VEC> &xr, const Pack<T, VEC> &zr, float (&v)[VEC]) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                v[i] = to_f32(xr.v[i]);
-                if (z && !p.norm_before_gate) v[i] *= silu(to_f32(zr.v[i]));
-            }
-        };
+        auto scale_of = [&](float sum) { return 1.0f / sqrtf(part_sum(sum, lanes, waves) / (float)p.group_dim + p.eps); };
+        const u32x4 none = {0u, 0u, 0u, 0u};
         if constexpr (HELD > 0) {
-            Pack<T, VEC> xr[HELD], zr[HELD];
+            // A piece that would pass the part's end is moved back to end
+            // there.  The elements it then shares with the piece before it
+            // are left out of the sum and stored twice with equal values
+            // (after every lane's loads: the scale depends on them all).
+            int at[HELD];
+            u32x4 xr[HELD], zr[HELD];
 #pragma unroll
             for (int m = 0; m < HELD; ++m) {
-                const int c = (m * lanes + lane) * VEC;
-                xr[m] = load_piece<T, VEC>(x + c, max(p.group_dim - c, 0));
-                if (z) zr[m] = load_piece<T, VEC>(z + c, max(p.group_dim - c, 0));
+                at[m] = min((m * lanes + lane) * VEC, p.group_dim - VEC);
+                xr[m] = load_words(x + at[m]);
+                zr[m] = z ? load_words(z + at[m]) : none;
             }
             float v[HELD][VEC], sum = 0.0f;
 #pragma unroll
             for (int m = 0; m < HELD; ++m) {
                 values(xr[m], zr[m], v[m]);
-                const int left = p.group_dim - (m * lanes + lane) * VEC;  // elements past the part's end count as 0
+                const int shared = (m * lanes + lane) * VEC - at[m];  // all of them: no piece of its own
+                if (shared == 0) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) sum = i < left ? fmaf(v[m][i], v[m][i], sum) : sum;
+                    for (int i = 0; i < VEC; ++i) sum = fmaf(v[m][i], v[m][i], sum);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) sum = i >= shared ? fmaf(v[m][i], v[m][i], sum) : sum;
+                }
             }
-            const float scale = 1.0f / sqrtf(part_sum(sum, lanes, waves) / (float)p.group_dim + p.eps);
+            const float scale = scale_of(sum);
 #pragma unroll
             for (int m = 0; m < HELD; ++m) {
-                const int c = (m * lanes + lane) * VEC;
-                if (c < p.group_dim) finish(v[m], zr[m], scale, c);
+                if ((m * lanes + lane) * VEC - at[m] >= VEC || mine >= parts) continue;
+                u32x4 wv[VEC / 4] = {};
+                if (weight)
+#pragma unroll
+                    for (int i = 0; i < VEC / 4; ++i) wv[i] = load_words(weight + at[m] + 4 * i);
+                store_words(out + at[m], scaled(v[m], zr[m], wv, scale));
             }
         } else {
+            // Whole pieces in a loop, the last, partial one by its lane.
+            const int whole = p.group_dim / VEC * VEC, left = p.group_dim - whole;
+            const bool last = left > 0 && (whole / VEC & (lanes - 1)) == lane;
             float v[VEC], sum = 0.0f;
-            auto piece = [&](int c) {
-                Pack<T, VEC> zr = {};
-                if (z) zr = load_piece<T, VEC>(z + c, p.group_dim - c);
-                values(load_piece<T, VEC>(x + c, p.group_dim - c), zr, v);
-                return zr;
-            };
-            for (int c = lane * VEC; c < p.group_dim; c += lanes * VEC) {
-                piece(c);
+            for (int c = lane * VEC; c < whole; c += lanes * VEC) {
+                values(load_words(x + c), z ? load_words(z + c) : none, v);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) sum = c + i < p.group_dim ? fmaf(v[i], v[i], sum) : sum;
+                for (int i = 0; i < VEC; ++i) sum = fmaf(v[i], v[i], sum);
             }
-            const float scale = 1.0f / sqrtf(part_sum(sum, lanes, waves) / (float)p.group_dim + p.eps);
-            for (int c = lane * VEC; c < p.group_dim; c += lanes * VEC) {
-                const Pack<T, VEC> zr = piece(c);
-                finish(v, zr, scale, c);
+            if (last) {
+                values(load_first(x + whole, left), z ? load_first(z + whole, left) : none, v);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sum = i < left ? fmaf(v[i], v[i], sum) : sum;
+            }
+            const float scale = scale_of(sum);
+            if (mine >= parts) continue;
+            for (int c = lane * VEC; c < whole; c += lanes * VEC) {
+                const u32x4 zr = z ? load_words(z + c) : none;
+                values(load_words(x + c), zr, v);
+                u32x4 wv[VEC / 4] = {};
+                if (weight)
+#pragma unroll
+                    for (int i = 0; i < VEC / 4; ++i) wv[i] = load_words(weight + c + 4 * i);
+                store_words(out + c, scaled(v, zr, wv, scale));
+            }
+            if (last) {
+                const u32x4 zr = z ? load_first(z + whole, left) : none;
+                values(load_first(x + whole, left), zr, v);
+                u32x4 wv[VEC / 4] = {};
+                if (weight)
+#pragma unroll
+                    for (int i = 0; i < VEC / 4; ++i)
+                        if (4 * i < left) wv[i] = load_first(weight + whole + 4 * i, left - 4 * i);
+                store_first(out + whole, scaled(v, zr, wv, scale), left);
             }
         }
     }
@@ -148,12 +165,14 @@ template <typename T>
 hipError_t run(const NormParams &p, hipStream_t stream) {
     constexpr int VEC = 16 / sizeof(T);
     const int pieces = (p.group_dim + VEC - 1) / VEC;
-    // The fewest lanes whose registers hold a part; at least 8.
+    // The fewest lanes whose registers hold a part (at least 8), and more
+    // while that leaves less than four waves per compute unit.
+    const int64_t parts = p.rows * p.ngroups;
     NormGrid gr = {8};
     while (gr.lanes < 1024 && (pieces + gr.lanes - 1) / gr.lanes > kMaxHeld) gr.lanes *= 2;
-    const int held = (pieces + gr.lanes - 1) / gr.lanes;
+    while (gr.lanes < 1024 && pieces > gr.lanes && parts * gr.lanes < 4 * 256 * 64) gr.lanes *= 2;
+    const int held = p.group_dim < VEC ? 0 : (pieces + gr.lanes - 1) / gr.lanes;
     const int threads = std::max(gr.lanes, 64);
-    const int64_t parts = p.rows * p.ngroups;
     const int64_t wgs = (parts * gr.lanes + threads - 1) / threads;
     const unsigned grid = (unsigned)std::min<int64_t>(wgs, (int64_t)1 << 22);
     switch (held) {

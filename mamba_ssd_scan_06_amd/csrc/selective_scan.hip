@@ -39,17 +39,24 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kCh = 8;         // channels per thread in the per-(token, channel) work
 static_assert(kTile * kChannels == kThreads * kCh, "one row piece per thread");
 
+// 8 channels of one token as loaded: 16 bytes of bf16, 32 of fp32.
 template <typename T>
-struct Row8 {  // 8 channels of one token as loaded
-    Pack<T, 8> v;
-    __device__ __forceinline__ void load(const T *p, int valid) {
-        if (valid == 8) {
-            v = *reinterpret_cast<const Pack<T, 8> *>(p);
-        } else {
+struct Row8 {
+    static constexpr int W = sizeof(T) * 8 / 16, VEC = 16 / sizeof(T);
+    u32x4 v[W];
+    __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v.v[i] = i < valid ? p[i] : from_f32<T>(0.0f);
+        for (int k = 0; k < W; ++k) v[k] = load_words(p + k * VEC);
+    }
+    // Element by element, the last of `valid` repeated.
+    __device__ __forceinline__ void load(const T *p, int valid) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            const int at = min(k * VEC, valid - 1);
+            v[k] = load_first(p + at, valid - at);
         }
     }
+    __device__ __forceinline__ float f32(int i) const { return word_f32(v[i / VEC], i % VEC, T()); }
 };
 
 // The accepted index of sequence b, clamped; seqlen where none is asked for.
@@ -59,8 +66,9 @@ __device__ __forceinline__ int64_t accepted(const SelectiveParams &p, int64_t b)
     return j < -1 ? -1 : (j > p.seqlen - 1 ? p.seqlen - 1 : j);
 }
 
-// STATES: leave the range's final state and sum of steps only.
-template <typename T, int N, bool STATES>
+// STATES: leave the range's final state and sum of steps only.  ODD: a group's
+// channels are no multiple of 8, so that rows are read element by element.
+template <typename T, int N, bool STATES, bool ODD>
 __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p) {
     constexpr int NS = N / kWaves;        // states per lane
     constexpr int BCV = 2 * N / 4;        // 4-element pieces of a token's B and C
@@ -84,9 +92,12 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     // This thread's 8 channels of one token of a tile.
     const int row = tid >> 3, c8 = (tid & 7) * kCh;
     const int nv = max(0, min(kCh, nch - c8));
-    const T *u = reinterpret_cast<const T *>(p.u) + b * p.u_bs + d0 + c8;
-    const T *dl = reinterpret_cast<const T *>(p.delta) + b * p.delta_bs + d0 + c8;
-    const T *z = !STATES && p.z ? reinterpret_cast<const T *>(p.z) + b * p.z_bs + d0 + c8 : nullptr;
+    // Where they are read: pieces past the tile's channels read its last
+    // channels again, and nothing comes of them.
+    const int from = d0 + (ODD ? min(c8, nch - 1) : min(c8, nch - kCh)), nread = ODD ? max(nv, 1) : kCh;
+    const T *u = reinterpret_cast<const T *>(p.u) + b * p.u_bs + from;
+    const T *dl = reinterpret_cast<const T *>(p.delta) + b * p.delta_bs + from;
+    const T *z = !STATES && p.z ? reinterpret_cast<const T *>(p.z) + b * p.z_bs + from : nullptr;
     const T *B = reinterpret_cast<const T *>(p.B) + b * p.B_bs + g * N;
     const T *C = reinterpret_cast<const T *>(p.C) + b * p.C_bs + g * N;
     float bias[kCh], skip[kCh];
@@ -96,20 +107,27 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
         skip[i] = !STATES && p.D && i < nv ? p.D[d0 + c8 + i] : 0.0f;
     }
 
+    // A tile's loads, none of them conditional so that they stay in flight.
+    // Tokens past the range's end read its last row again (the scan stops
+    // before them).
     Row8<T> ru, rd, rz;
     Pack<T, 4> rbc[BCT];
     auto load_tile = [&](int64_t t0) {
-        const int64_t t = t0 + row;
-        const int valid = t < t_hi ? nv : 0;
-        ru.load(u + t * p.u_ts, valid);
-        rd.load(dl + t * p.delta_ts, valid);
-        if (z) rz.load(z + t * p.z_ts, valid);
+        const int64_t t = min(t0 + row, t_hi - 1);
+        if constexpr (ODD) {
+            ru.load(u + t * p.u_ts, nread);
+            rd.load(dl + t * p.delta_ts, nread);
+            if (z) rz.load(z + t * p.z_ts, nread);
+        } else {
+            ru.load(u + t * p.u_ts);
+            rd.load(dl + t * p.delta_ts);
+            if (z) rz.load(z + t * p.z_ts);
+        }
 #pragma unroll
         for (int k = 0; k < BCT; ++k) {
-            const int e = tid + k * kThreads, tr = e / BCV, c = (e - tr * BCV) * 4;
-            if (e < kTile * BCV && t0 + tr < t_hi)
-                rbc[k] = *reinterpret_cast<const Pack<T, 4> *>(c < N ? B + (t0 + tr) * p.B_ts + c
-                                                                     : C + (t0 + tr) * p.C_ts + c - N);
+            const int e = min(tid + k * kThreads, kTile * BCV - 1), tr = e / BCV, c = (e - tr * BCV) * 4;
+            const int64_t tb = min(t0 + tr, t_hi - 1);
+            rbc[k] = *reinterpret_cast<const Pack<T, 4> *>(c < N ? B + tb * p.B_ts + c : C + tb * p.C_ts + c - N);
         }
     };
     load_tile(t_lo);
@@ -125,9 +143,9 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     {
         // Range 0 of the full pass takes init_state from the first launch's
         // copy: the last range may be writing final_state over it by now.
-        const float *from = !STATES && p.ranges > 1 ? p.range_state + (int64_t)(p.ranges - 1) * slot : p.init_state;
+        const float *first = !STATES && p.ranges > 1 ? p.range_state + (int64_t)(p.ranges - 1) * slot : p.init_state;
 #pragma unroll
-        for (int n = 0; n < NS; ++n) h[n] = mine && p.init_state && r == 0 ? from[at + n] : 0.0f;
+        for (int n = 0; n < NS; ++n) h[n] = mine && p.init_state && r == 0 ? first[at + n] : 0.0f;
     }
     if (STATES) {
         if (r == 0 && p.init_state && mine)
@@ -158,8 +176,8 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
             f32x4 dv[2], du[2];
 #pragma unroll
             for (int i = 0; i < kCh; ++i) {
-                uv[i] = to_f32(ru.v.v[i]);
-                float s = to_f32(rd.v.v[i]) + bias[i];
+                uv[i] = ru.f32(i);
+                float s = rd.f32(i) + bias[i];
                 if (p.softplus) s = softplus(s);
                 dv[i >> 2][i & 3] = s;
                 du[i >> 2][i & 3] = s * uv[i];
@@ -224,17 +242,17 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
                 for (int i = 0; i < 4; ++i) {
                     const int c = 4 * q + i;
                     float f = fmaf(skip[c], uv[c], v[i]);
-                    if (z) f *= silu(to_f32(zc.v.v[c]));
+                    if (z) f *= silu(zc.f32(c));
                     o.v[c] = from_f32<T>(f);
                 }
             }
             T *yr = y + t0 * p.channels;
-            if (nv == kCh) {
-                *reinterpret_cast<Pack<T, kCh> *>(yr) = o;
-            } else {
+            if constexpr (ODD) {
 #pragma unroll
                 for (int i = 0; i < kCh; ++i)
                     if (i < nv) yr[i] = o.v[i];
+            } else {
+                *reinterpret_cast<Pack<T, kCh> *>(yr) = o;
             }
         }
     }
@@ -312,24 +330,29 @@ __global__ __launch_bounds__(kThreads) void scan_steps_kernel(SelectiveParams p)
 // Calls up to this many tokens run without tiles.
 constexpr int64_t kFewTokens = 16;
 
+template <typename T, int N, bool ODD>
+hipError_t run_tiles(const SelectiveParams &p, hipStream_t stream) {
+    const unsigned tiles = (p.group_channels + kChannels - 1) / kChannels;
+    if (p.ranges > 1) {
+        const dim3 grid(tiles * (p.ranges - 1), p.ngroups, (unsigned)p.batch);
+        scan_tiles_kernel<T, N, true, ODD><<<grid, kThreads, 0, stream>>>(p);
+        const hipError_t r = hipGetLastError();
+        if (r != hipSuccess) return r;
+    }
+    const dim3 grid(tiles * p.ranges, p.ngroups, (unsigned)p.batch);
+    scan_tiles_kernel<T, N, false, ODD><<<grid, kThreads, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
 template <typename T, int N>
-hipError_t run(SelectiveParams p, hipStream_t stream) {
+hipError_t run(const SelectiveParams &p, hipStream_t stream) {
     if (p.seqlen <= kFewTokens) {
         constexpr int CH = kThreads / (N / 4);
         const dim3 grid((p.group_channels + CH - 1) / CH, p.ngroups, (unsigned)p.batch);
         scan_steps_kernel<T, N><<<grid, kThreads, 0, stream>>>(p);
         return hipGetLastError();
     }
-    const unsigned tiles = (p.group_channels + kChannels - 1) / kChannels;
-    if (p.ranges > 1) {
-        const dim3 grid(tiles * (p.ranges - 1), p.ngroups, (unsigned)p.batch);
-        scan_tiles_kernel<T, N, true><<<grid, kThreads, 0, stream>>>(p);
-        const hipError_t r = hipGetLastError();
-        if (r != hipSuccess) return r;
-    }
-    const dim3 grid(tiles * p.ranges, p.ngroups, (unsigned)p.batch);
-    scan_tiles_kernel<T, N, false><<<grid, kThreads, 0, stream>>>(p);
-    return hipGetLastError();
+    return p.group_channels % kCh == 0 ? run_tiles<T, N, false>(p, stream) : run_tiles<T, N, true>(p, stream);
 }
 
 template <typename T>

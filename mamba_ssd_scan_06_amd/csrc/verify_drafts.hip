@@ -24,7 +24,18 @@ constexpr int kSumThreads = 256;
 constexpr int kMaxSegments = 64;
 
 // A probability's mass: NaN and negative values count as none.
-__device__ __forceinline__ double mass(double v) { return v > 0.0 ? v : 0.0; }
+__device__ __forceinline__ double mass(double v) { return __builtin_fmax(v, 0.0); }
+
+// Inclusive prefix sums over a wave's lanes.
+__device__ __forceinline__ double lane_prefix(double v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+        const double o = __shfl_up(v, k);
+        if (lane >= k) v += o;
+    }
+    return v;
+}
 
 // What a sequence's drafts leave: the row to draw from.
 template <typename T>
@@ -158,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyParams p) {
         if (tid < segments) sums[tid] = p.sums[b * segments + tid];
         __syncthreads();
     }
-    double total = 0.0;
+    double total = 0.0, own = 0.0, upto = 0.0;
     for (int pass = 0; pass < 2; ++pass) {
         if (p.segments == 1 || pass == 1) {
             segments = kWaves;
@@ -167,8 +178,10 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyParams p) {
             if (lane == 0) sums[wave] = s;
             __syncthreads();
         }
-        total = 0.0;
-        for (int k = 0; k < segments; ++k) total += sums[k];
+        // Every wave forms the same prefix over the segments, one per lane.
+        own = lane < segments ? sums[lane] : 0.0;
+        upto = lane_prefix(own);
+        total = __shfl(upto, 63);
         if (total > 0.0 || !r.drawn) break;
         // Rounding left the residual without mass: p_n takes its place.
         r.drawn = false;
@@ -179,17 +192,9 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyParams p) {
     const double cut = (double)p.u[b * (K + 1) + K] * total;
     // The segment with the cut: the first whose end passes it, or the last
     // with mass (a uniform outside [0,1), rounding).
-    int seg = -1;
-    double before = 0.0, run = 0.0;
-    for (int k = 0; k < segments; ++k) {
-        const double end = run + sums[k];
-        if (sums[k] > 0.0) {
-            seg = k;
-            before = run;
-            if (end > cut) break;
-        }
-        run = end;
-    }
+    const uint64_t some = __ballot(own > 0.0), past = __ballot(own > 0.0 && upto > cut);
+    const int seg = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : -1;
+    double before = seg > 0 ? __shfl(upto, seg - 1) : 0.0;
     int next = (int)(V - 1);  // a row without mass
     if (seg >= 0) {
         if (tid == 0) {
@@ -199,15 +204,15 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyParams p) {
         const int64_t lo = seg * segment, hi = min(lo + segment, V), per = (hi - lo + kThreads - 1) / kThreads;
         const int64_t a = min(lo + tid * per, hi), e = min(a + per, hi);
         double s = 0.0;
+#pragma unroll 4
         for (int64_t v = a; v < e; ++v) s += r.at(v);
-        double pre = s;  // inclusive prefix over the wave's lanes
-        for (int k = 1; k < 64; k <<= 1) {
-            const double o = __shfl_up(pre, k);
-            if (lane >= k) pre += o;
-        }
+        const double pre = lane_prefix(s);
         if (lane == 63) wave_sums[wave] = pre;
         __syncthreads();
-        for (int w = 0; w < wave; ++w) before += wave_sums[w];
+        {
+            const double ends = lane_prefix(lane < kWaves ? wave_sums[lane] : 0.0);
+            if (wave > 0) before += __shfl(ends, wave - 1);
+        }
         if (s > 0.0) {
             // This thread's elements, from the sum before them.
             double at = before + (pre - s);
