@@ -464,7 +464,7 @@ typedef struct {
  * fp64 in a fixed order, so equal inputs give equal tokens.  Without
  * draft_probs every q_i is 1 at tok_i and 0 elsewhere (looked-up drafts).
  * Where rounding left r without mass, p_n takes its place; a row without mass
- * gives V-1; NaN and negative probabilities count as no mass.
+ * gives V-1; NaN and negative probabilities count as 0.
  *
  *   target_probs  [b,K+1,V]  dtype  strided; row i judges draft i
  *   draft_probs   [b,K,V]    dtype  strided; NULL = as above

@@ -10,31 +10,56 @@
 // Only the K tested probabilities and one row of p and q are needed.  A row is
 // summed in segments; the prefix over their sums finds the segment that holds
 // the cut, which is read again (from cache) with a few adjacent elements per
-// thread.  With many sequences a workgroup of 16 waves takes a whole row, its
-// waves' pieces being the segments; with few, a first launch sums the segments
-// of all rows on the whole GPU and a workgroup per row picks the token.
+// thread.  A workgroup of eight waves takes a whole row, its waves' pieces
+// being the segments; where rows are few and long, a first launch sums the
+// segments of all rows on the whole GPU and a workgroup per row picks the
+// token (verify_segments).  What is left is a chain of latencies: the tested
+// probabilities 1 us, a round of a row's loads 1.25 us each (7.8 us of 15.7
+// for 256 rows of 50277), two barriers and the segment again 2 us.
 #include "device_common.hpp"
 #include "kernels.hpp"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kSumThreads = 256;
-constexpr int kMaxSegments = 64;
+constexpr int kMaxSegments = 64;  // one per lane
+constexpr int kEach = 8;          // elements per thread when a segment is read again
 
-// A probability's mass: NaN and negative values count as none.
-__device__ __forceinline__ double mass(double v) { return __builtin_fmax(v, 0.0); }
+// A probability as it counts: NaN and negative values as 0.
+__device__ __forceinline__ float clean(float v) { return __builtin_amdgcn_fmed3f(v, 0.0f, __builtin_inff()); }
+// max(p - q, 0) of a cleaned p and any q as p minus the median of p, q and 0
+// (min(p, q) for q >= 0; 0 for a negative or NaN q).  Two fp32 values differ
+// by an fp64 one exactly, or to 2^-53 of it.
+__device__ __forceinline__ double rest(float p, float q) {
+    return (double)p - (double)__builtin_amdgcn_fmed3f(p, q, 0.0f);
+}
 
-// Inclusive prefix sums over a wave's lanes.
+// v plus the value a DPP control moves here (0 where it moves none).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double plus_moved(double v) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    const i32x2 x = __builtin_bit_cast(i32x2, v);
+    const int lo = __builtin_amdgcn_update_dpp(0, x[0], CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, x[1], CTRL, ROWS, 0xf, false);
+    return v + __builtin_bit_cast(double, i32x2{lo, hi});
+}
+// Inclusive prefix sums over a wave's 64 lanes: shifts within rows of 16, then
+// each row's last lane into the rows after it.
 __device__ __forceinline__ double lane_prefix(double v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) {
-        const double o = __shfl_up(v, k);
-        if (lane >= k) v += o;
-    }
-    return v;
+    v = plus_moved<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+    v = plus_moved<0x112, 0xf>(v);
+    v = plus_moved<0x114, 0xf>(v);
+    v = plus_moved<0x118, 0xf>(v);
+    v = plus_moved<0x142, 0xa>(v);  // row_bcast 15 into rows 1 and 3
+    return plus_moved<0x143, 0xc>(v);  // row_bcast 31 into rows 2 and 3
+}
+// Lane `lane`'s value, the same for the whole wave.
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    const i32x2 x = __builtin_bit_cast(i32x2, v);
+    return __builtin_bit_cast(double, i32x2{__builtin_amdgcn_readlane(x[0], lane), __builtin_amdgcn_readlane(x[1], lane)});
 }
 
 // What a sequence's drafts leave: the row to draw from.
@@ -45,45 +70,62 @@ struct Residual {
     bool drawn;       // a draft was rejected: r is the residual, not p itself
 
     __device__ __forceinline__ double at(int64_t v) const {
-        const double pv = (double)to_f32(p[v]);
-        if (q) return mass(pv - (double)to_f32(q[v]));
-        return v == zeroed ? 0.0 : mass(pv);
+        const float f = v == zeroed ? 0.0f : clean(to_f32(p[v]));
+        return q ? rest(f, to_f32(q[v])) : (double)f;
     }
-    // Sum over [lo, hi) by the 64 lanes of a wave, each adding 16 bytes of
-    // elements at a time; the same in every lane.
-    __device__ __forceinline__ double wave_sum(int64_t lo, int64_t hi) const {
-        constexpr int VEC = 16 / sizeof(T);
-        const int lane = threadIdx.x & 63;
-        double s = 0.0;
-        int64_t v = lo + lane * VEC;
-        auto add = [&](const Pack<T, VEC> &pv, const Pack<T, VEC> &qv, int64_t from) {
+    // x[i] = at(v + i); loads first, then their uses.  Beyond `end` x is any value.
+    __device__ __forceinline__ void read(int64_t v, int64_t end, double (&x)[kEach]) const {
+        constexpr int VEC = 16 / sizeof(T), W = kEach / VEC;
+        if (end < kEach) {
+            for (int i = 0; i < kEach; ++i) x[i] = at(min(v + i, end - 1));
+            return;
+        }
+        u32x4 pv[W], qv[W];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const double d = (double)to_f32(pv.v[i]);
-                s += q ? mass(d - (double)to_f32(qv.v[i])) : from + i == zeroed ? 0.0 : mass(d);
-            }
-        };
-        constexpr int STEP = 64 * VEC, U = 4;
-        for (; v + (U - 1) * STEP + VEC <= hi; v += U * STEP) {
-            Pack<T, VEC> pv[U], qv[U];
+        for (int k = 0; k < W; ++k) pv[k] = load_words(p + v + k * VEC);
+        if (q) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) qv[k] = load_words(q + v + k * VEC);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                x[i] = rest(clean(word_f32(pv[i / VEC], i % VEC, T())), word_f32(qv[i / VEC], i % VEC, T()));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                x[i] = v + i == zeroed ? 0.0 : (double)clean(word_f32(pv[i / VEC], i % VEC, T()));
+        }
+    }
+    // Sum over [lo, hi) by the 64 lanes of a wave, the same in every lane.
+    __device__ __forceinline__ double wave_sum(int64_t lo, int64_t hi) const {
+        double s = 0.0;
+        if (lo < hi) s = q ? lane_sum<true>(lo, (int)(hi - lo)) : lane_sum<false>(lo, (int)(hi - lo));
+        return lane_value(lane_prefix(s), 63);
+    }
+    // One lane's share: adjacent lanes read adjacent elements, 16 rounds of
+    // them in flight (none conditional): any alignment of the row is as good
+    // as another, and the body stays small (it runs a few times per launch).
+    template <bool Q>
+    __device__ __forceinline__ double lane_sum(int64_t lo, int len) const {
+        constexpr int U = 16;
+        const T *pl = p + lo, *ql = Q ? q + lo : nullptr;
+        const int z = zeroed >= lo && zeroed < lo + len ? (int)(zeroed - lo) : -1;
+        double s = 0.0;
+#pragma unroll 1
+        for (int at = threadIdx.x & 63; at < len; at += 64 * U) {
+            T pv[U], qv[U];
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                pv[k] = *reinterpret_cast<const Pack<T, VEC> *>(p + v + k * STEP);
-                if (q) qv[k] = *reinterpret_cast<const Pack<T, VEC> *>(q + v + k * STEP);
+                const int v = min(at + 64 * k, len - 1);
+                pv[k] = pl[v];
+                if (Q) qv[k] = ql[v];
             }
 #pragma unroll
-            for (int k = 0; k < U; ++k) add(pv[k], qv[k], v + k * STEP);
-        }
-        for (; v < hi; v += STEP) {
-            if (v + VEC <= hi) {
-                Pack<T, VEC> pv = *reinterpret_cast<const Pack<T, VEC> *>(p + v), qv = {};
-                if (q) qv = *reinterpret_cast<const Pack<T, VEC> *>(q + v);
-                add(pv, qv, v);
-            } else {
-                for (int64_t k = v; k < hi; ++k) s += at(k);
+            for (int k = 0; k < U; ++k) {
+                const int v = at + 64 * k;
+                const float f = v < len && v != z ? clean(to_f32(pv[k])) : 0.0f;
+                s += Q ? rest(f, to_f32(qv[k])) : (double)f;
             }
         }
-        for (int m = 32; m > 0; m >>= 1) s += __shfl_xor(s, m);
         return s;
     }
 };
@@ -93,25 +135,27 @@ __device__ __forceinline__ int drafts_of(const VerifyParams &p, int64_t b) {
     return m < 0 ? 0 : (m > p.drafts ? p.drafts : m);
 }
 
-// The number of accepted drafts of sequence b, by all threads of a workgroup;
-// *first is LDS.
+// The number of accepted drafts of sequence b: every wave tests them all, 64
+// at a time, so that no wave waits for another.
 template <typename T>
-__device__ __forceinline__ int accepted_drafts(const VerifyParams &p, int64_t b, int m, int *first) {
-    if (threadIdx.x == 0) *first = m;
-    __syncthreads();
-    for (int i = threadIdx.x; i < m; i += blockDim.x) {
-        const int32_t v = p.tok[b * p.drafts + i];
-        bool ok = v >= 0 && v < p.vocab;
-        if (ok) {
-            const double q =
-                p.draft ? (double)to_f32(reinterpret_cast<const T *>(p.draft)[b * p.d_bs + i * p.d_rs + v]) : 1.0;
-            ok = (double)p.u[b * (p.drafts + 1) + i] * q <
-                 (double)to_f32(reinterpret_cast<const T *>(p.target)[b * p.t_bs + i * p.t_rs + v]);
+__device__ __forceinline__ int accepted_drafts(const VerifyParams &p, int64_t b, int m) {
+    for (int i0 = 0; i0 < m; i0 += 64) {
+        const int i = i0 + (threadIdx.x & 63);
+        bool ok = true;
+        if (i < m) {
+            const int32_t v = p.tok[b * p.drafts + i];
+            ok = v >= 0 && v < p.vocab;
+            if (ok) {
+                const float q =
+                    p.draft ? clean(to_f32(reinterpret_cast<const T *>(p.draft)[b * p.d_bs + i * p.d_rs + v])) : 1.0f;
+                ok = (double)p.u[b * (p.drafts + 1) + i] * (double)q <
+                     (double)clean(to_f32(reinterpret_cast<const T *>(p.target)[b * p.t_bs + i * p.t_rs + v]));
+            }
         }
-        if (!ok) atomicMin(first, i);
+        const uint64_t rejects = __ballot(!ok);
+        if (rejects) return i0 + __builtin_ctzll(rejects);
     }
-    __syncthreads();
-    return *first;
+    return m;
 }
 
 template <typename T>
@@ -127,10 +171,9 @@ __device__ __forceinline__ Residual<T> residual_of(const VerifyParams &p, int64_
 // First launch of a split call: n_accepted and the segments' sums.
 template <typename T>
 __global__ __launch_bounds__(kSumThreads) void verify_sums_kernel(VerifyParams p) {
-    __shared__ int first;
     __shared__ double part[kSumThreads / 64];
     const int64_t b = blockIdx.y;
-    const int m = drafts_of(p, b), n = accepted_drafts<T>(p, b, m, &first);
+    const int m = drafts_of(p, b), n = accepted_drafts<T>(p, b, m);
     const Residual<T> r = residual_of<T>(p, b, n, m);
     const int64_t lo = blockIdx.x * p.segment, hi = min(lo + p.segment, p.vocab);
     constexpr int NW = kSumThreads / 64;
@@ -151,15 +194,17 @@ __global__ __launch_bounds__(kSumThreads) void verify_sums_kernel(VerifyParams p
 template <typename T>
 __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyParams p) {
     __shared__ double sums[kMaxSegments], wave_sums[kWaves];
-    __shared__ int first, found, last_mass;
+    __shared__ int wave_hit[kWaves], wave_last[kWaves];
     const int64_t b = blockIdx.x, V = p.vocab;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, K = p.drafts;
+    const int tid = threadIdx.x, lane = tid & 63, K = p.drafts;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m = drafts_of(p, b);
+    const int32_t drafted = tid < K ? p.tok[b * K + tid] : -1;
     int n;
     if (p.segments > 1) {
         n = p.n_accepted[b];
     } else {
-        n = accepted_drafts<T>(p, b, m, &first);
+        n = accepted_drafts<T>(p, b, m);
         if (tid == 0) p.n_accepted[b] = n;
     }
     Residual<T> r = residual_of<T>(p, b, n, m);
@@ -181,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyParams p) {
         // Every wave forms the same prefix over the segments, one per lane.
         own = lane < segments ? sums[lane] : 0.0;
         upto = lane_prefix(own);
-        total = __shfl(upto, 63);
+        total = lane_value(upto, 63);
         if (total > 0.0 || !r.drawn) break;
         // Rounding left the residual without mass: p_n takes its place.
         r.drawn = false;
@@ -194,47 +239,65 @@ __global__ __launch_bounds__(kThreads) void verify_pick_kernel(VerifyParams p) {
     // with mass (a uniform outside [0,1), rounding).
     const uint64_t some = __ballot(own > 0.0), past = __ballot(own > 0.0 && upto > cut);
     const int seg = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : -1;
-    double before = seg > 0 ? __shfl(upto, seg - 1) : 0.0;
+    double before = seg > 0 ? lane_value(upto, seg - 1) : 0.0;
     int next = (int)(V - 1);  // a row without mass
     if (seg >= 0) {
-        if (tid == 0) {
-            found = 0x7fffffff;
-            last_mass = -1;
-        }
-        const int64_t lo = seg * segment, hi = min(lo + segment, V), per = (hi - lo + kThreads - 1) / kThreads;
-        const int64_t a = min(lo + tid * per, hi), e = min(a + per, hi);
-        double s = 0.0;
-#pragma unroll 4
-        for (int64_t v = a; v < e; ++v) s += r.at(v);
-        const double pre = lane_prefix(s);
-        if (lane == 63) wave_sums[wave] = pre;
-        __syncthreads();
-        {
-            const double ends = lane_prefix(lane < kWaves ? wave_sums[lane] : 0.0);
-            if (wave > 0) before += __shfl(ends, wave - 1);
-        }
-        if (s > 0.0) {
-            // This thread's elements, from the sum before them.
-            double at = before + (pre - s);
-            int last = -1;
-            for (int64_t v = a; v < e; ++v) {
-                const double x = r.at(v);
-                if (x > 0.0) last = (int)v;
-                at += x;
-                if (x > 0.0 && at > cut) {
-                    atomicMin(&found, (int)v);
-                    break;
-                }
+        const int64_t lo = seg * segment, hi = min(lo + segment, V);
+        // The segment again, kEach adjacent elements per thread at most.
+        int found = -1, last_mass = -1;
+        for (int64_t from = lo; from < hi; from += kThreads * kEach) {
+            const int64_t to = min(from + kThreads * kEach, hi);
+            const int each = (int)((to - from + kThreads - 1) / kThreads);
+            const int64_t a = from + tid * each;
+            // Read kEach elements from `at` on, moved back where they would
+            // pass the row's end; this thread's are those in [a, a + each).
+            const int64_t at = max(min(a, V - kEach), (int64_t)0);
+            double x[kEach], s = 0.0;
+            r.read(at, V, x);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                x[i] = at + i >= a && at + i < min(a + each, to) ? x[i] : 0.0;
+                s += x[i];
             }
-            atomicMax(&last_mass, last);
+            const double pre = lane_prefix(s);
+            if (lane == 63) wave_sums[wave] = pre;
+            __syncthreads();
+            const double ends = lane_prefix(lane < kWaves ? wave_sums[lane] : 0.0);
+            // This thread's elements, from the sum before them.
+            double sum = before + (wave > 0 ? lane_value(ends, wave - 1) : 0.0) + (pre - s);
+            int last = -1, hit = -1;
+#pragma unroll
+            for (int i = kEach - 1; i >= 0; --i) last = x[i] > 0.0 && last < 0 ? (int)(at + i) : last;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                sum += x[i];
+                if (x[i] > 0.0 && sum > cut && hit < 0) hit = (int)(at + i);
+            }
+            // The first lane with a hit and the last with mass, then the same
+            // over the waves (no atomics: one per lane on one address costs
+            // 5 us here).
+            const uint64_t hits = __ballot(hit >= 0), some_mass = __ballot(last >= 0);
+            if (lane == 0) {
+                wave_hit[wave] = -1;
+                wave_last[wave] = -1;
+            }
+            if (hits && lane == __builtin_ctzll(hits)) wave_hit[wave] = hit;
+            if (some_mass && lane == 63 - __builtin_clzll(some_mass)) wave_last[wave] = last;
+            before += lane_value(ends, kWaves - 1);
+            __syncthreads();
+            for (int w = kWaves - 1; w >= 0; --w) {
+                if (wave_hit[w] >= 0) found = wave_hit[w];
+                if (wave_last[w] > last_mass) last_mass = wave_last[w];
+            }
+            if (found >= 0) break;
+            __syncthreads();  // the next turn writes wave_sums and these again
         }
-        __syncthreads();
-        next = found != 0x7fffffff ? found : last_mass;
+        next = found >= 0 ? found : last_mass;
     }
     if (tid == 0) p.next_token[b] = next;
     if (p.tokens)
         for (int i = tid; i <= K; i += kThreads)
-            p.tokens[b * (K + 1) + i] = i < n ? p.tok[b * K + i] : i == n ? next : -1;
+            p.tokens[b * (K + 1) + i] = i < n ? (i == tid ? drafted : p.tok[b * K + i]) : i == n ? next : -1;
 }
 
 template <typename T>
@@ -251,10 +314,16 @@ hipError_t run(const VerifyParams &p, hipStream_t stream) {
 }  // namespace
 
 void verify_segments(VerifyParams &p) {
-    // Split while the rows alone leave compute units idle and a segment keeps
-    // at least 4096 elements (16 per thread of its workgroup).
-    const int64_t want = std::min<int64_t>({kMaxSegments, 256 / std::max<int64_t>(p.batch, 1), p.vocab / 4096});
-    p.segments = want >= 4 ? (int)want : 1;
+    // Segments for four workgroups per compute unit, of 2048 elements at least
+    // (half a round of a workgroup's loads).
+    const int64_t want = std::min<int64_t>({kMaxSegments, 1024 / std::max<int64_t>(p.batch, 1), p.vocab / 2048});
+    // Two launches pay where a row alone takes three rounds of its workgroup's
+    // loads (us with one launch / two: 1 row of 16384 8.0 / 8.2, of 32000 10.1 /
+    // 8.4, of 128256 21.9 / 7.9; 64 rows of 32000 10.6 / 11.1, of 64000 17.4 /
+    // 11.4) and the rows leave compute units idle (128 rows of 128256 32.9 /
+    // 32.2; 256 rows of 50277 15.7 / 22.6).
+    const int64_t rounds = p.vocab / (kThreads * 16);
+    p.segments = want >= 2 && rounds >= 3 && p.batch <= 64 ? (int)want : 1;
     p.segment = (p.vocab + p.segments - 1) / p.segments;
 }
 

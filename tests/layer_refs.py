@@ -136,6 +136,8 @@ def verify(p, tok, u, q=None, lens=None):
     """(n_accepted, next_token, tokens): p [b,K+1,V] fp64."""
     b, rows, V = p.shape
     K = rows - 1
+    p = np.where(p > 0, p, 0.0)                        # NaN and negative values count as 0
+    q = None if q is None else np.where(q > 0, q, 0.0)
     n_acc, nxt = np.zeros(b, np.int32), np.zeros(b, np.int32)
     tokens = np.full((b, rows), -1, np.int32)
     for i in range(b):
@@ -154,7 +156,7 @@ def verify(p, tok, u, q=None, lens=None):
                 r[tok[i, n]] = 0.0
         r = np.where(r > 0, r, 0.0)
         if n < m and not r.any():
-            r = np.where(p[i, n] > 0, p[i, n], 0.0)
+            r = p[i, n]
         cdf = np.cumsum(r)
         above = np.nonzero(cdf > u[i, K] * cdf[-1])[0]
         some = np.nonzero(r)[0]
