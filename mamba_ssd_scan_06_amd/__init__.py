@@ -483,10 +483,11 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, state_out_idx=Non
         final_state = x.new_empty(held)
     if state_out is None and state_out_idx is not None:
         state_out = x.new_empty(held)
-    pad = [0] * (3 - len(sizes))
-    shape = ssd_conv_shape(b, T, (ctypes.c_int64 * 3)(*sizes, *pad), w, st[0], st[1])
+    n = len(sizes)
+    shape = ssd_conv_shape(b, T, (*sizes, 0, 0)[:3], w, st[0], st[1])
     _check(lib.ssd_causal_conv_fwd(_addr(x), _addr(weight), _addr(bias), _addr(init_state),
-                                   1 if activation == "silu" else 0, *[_addr(o) for o in outs], *[None for _ in pad],
+                                   1 if activation == "silu" else 0, outs[0].data_ptr(),
+                                   outs[1].data_ptr() if n > 1 else None, outs[2].data_ptr() if n > 2 else None,
                                    _addr(final_state), _addr(state_out_idx), _addr(state_out), ctypes.byref(shape),
                                    code, _raw_stream(torch, dev)))
     return (outs[0] if split is None else tuple(outs)), final_state, state_out

@@ -131,6 +131,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, unsigned run, int 
         return to_words(r, T());
     };
     out += b * T_len * width;
+    wait_vmcnt<0>();  // weights and history: the loop then waits for its own loads one by one
     int64_t t = t0;
     for (; t + kBatchLoads <= t1; t += kBatchLoads) {
         u32x4 v[kBatchLoads];

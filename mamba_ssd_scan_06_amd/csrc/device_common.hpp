@@ -48,20 +48,18 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.0f + exp2_hw(-v * kLog2e)); }
 // log(1 + e^x) with full relative accuracy, also where it is small: with e =
 // exp(-|x|) in (0, 1] and r = e / (2 + e) in (0, 1/3], log(1 + e) = 2 atanh(r)
-// = 2 r (1 + r^2/3 + r^4/5 + ...); eight terms leave (1/9)^8 / 17 = 1.4e-9.
+// = 2 r P(r^2).  P is the Chebyshev interpolant of atanh(sqrt q) / sqrt q of
+// degree 4 on [0, 1/9]: 4e-9 off at most.
 __device__ __forceinline__ float softplus(float x) {
     const float e = exp2_hw(-fabsf(x) * kLog2e);
     const float r = e * __builtin_amdgcn_rcpf(2.0f + e);
     const float q = r * r;
-    float s = 1.0f / 15.0f;
-    s = fmaf(s, q, 1.0f / 13.0f);
-    s = fmaf(s, q, 1.0f / 11.0f);
-    s = fmaf(s, q, 1.0f / 9.0f);
-    s = fmaf(s, q, 1.0f / 7.0f);
-    s = fmaf(s, q, 1.0f / 5.0f);
-    s = fmaf(s, q, 1.0f / 3.0f);
+    float s = 0.140873286f;
+    s = fmaf(s, q, 0.139807094f);
+    s = fmaf(s, q, 0.200124269f);
+    s = fmaf(s, q, 0.333331580f);
     s = fmaf(s, q, 1.0f);
-    return fmaxf(x, 0.0f) + 2.0f * r * s;
+    return fmaf(r + r, s, fmaxf(x, 0.0f));
 }
 
 __device__ __forceinline__ float to_f32(bf16 v) { return (float)v; }

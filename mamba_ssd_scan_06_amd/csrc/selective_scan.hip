@@ -97,7 +97,8 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     const int from = d0 + (ODD ? min(c8, nch - 1) : min(c8, nch - kCh)), nread = ODD ? max(nv, 1) : kCh;
     const T *u = reinterpret_cast<const T *>(p.u) + b * p.u_bs + from;
     const T *dl = reinterpret_cast<const T *>(p.delta) + b * p.delta_bs + from;
-    const T *z = !STATES && p.z ? reinterpret_cast<const T *>(p.z) + b * p.z_bs + from : nullptr;
+    const bool gated = !STATES && p.z != nullptr;
+    const T *z = reinterpret_cast<const T *>(p.z) + (gated ? b * p.z_bs + from : 0);
     const T *B = reinterpret_cast<const T *>(p.B) + b * p.B_bs + g * N;
     const T *C = reinterpret_cast<const T *>(p.C) + b * p.C_bs + g * N;
     float bias[kCh], skip[kCh];
@@ -113,21 +114,25 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     Row8<T> ru, rd, rz;
     Pack<T, 4> rbc[BCT];
     auto load_tile = [&](int64_t t0) {
-        const int64_t t = min(t0 + row, t_hi - 1);
+        const int left = (int)min(t_hi - t0, (int64_t)kTile) - 1;  // last token of the tile
+        const int tr = min(row, left);
+        const T *pu = u + t0 * p.u_ts + tr * p.u_ts, *pd = dl + t0 * p.delta_ts + tr * p.delta_ts,
+                *pz = z + t0 * p.z_ts + tr * p.z_ts;
         if constexpr (ODD) {
-            ru.load(u + t * p.u_ts, nread);
-            rd.load(dl + t * p.delta_ts, nread);
-            if (z) rz.load(z + t * p.z_ts, nread);
+            ru.load(pu, nread);
+            rd.load(pd, nread);
+            if (gated) rz.load(pz, nread);
         } else {
-            ru.load(u + t * p.u_ts);
-            rd.load(dl + t * p.delta_ts);
-            if (z) rz.load(z + t * p.z_ts);
+            ru.load(pu);
+            rd.load(pd);
+            if (gated) rz.load(pz);
         }
+        const T *Bt = B + t0 * p.B_ts, *Ct = C + t0 * p.C_ts;
 #pragma unroll
         for (int k = 0; k < BCT; ++k) {
-            const int e = min(tid + k * kThreads, kTile * BCV - 1), tr = e / BCV, c = (e - tr * BCV) * 4;
-            const int64_t tb = min(t0 + tr, t_hi - 1);
-            rbc[k] = *reinterpret_cast<const Pack<T, 4> *>(c < N ? B + tb * p.B_ts + c : C + tb * p.C_ts + c - N);
+            const int e = min(tid + k * kThreads, kTile * BCV - 1), c = e % BCV * 4;
+            const int tb = min(e / BCV, left);
+            rbc[k] = *reinterpret_cast<const Pack<T, 4> *>(c < N ? Bt + tb * p.B_ts + c : Ct + tb * p.C_ts + c - N);
         }
     };
     load_tile(t_lo);
@@ -152,12 +157,22 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
 #pragma unroll
             for (int n = 0; n < NS; ++n) p.range_state[(int64_t)(p.ranges - 1) * slot + at + n] = h[n];
     } else if (r > 0 && mine) {
-#pragma unroll 4
-        for (int k = 0; k < r; ++k) {
-            const float sum = p.range_steps[((int64_t)k * p.batch + b) * p.channels + d0 + lane];
+        constexpr int U = NS > 8 ? 4 : 8;  // ranges whose loads are in flight together
+        const float *st = p.range_state + at, *su = p.range_steps + b * p.channels + d0 + lane;
+        for (int k0 = 0; k0 < r; k0 += U) {
+            float sum[U], hr[U][NS];
 #pragma unroll
-            for (int n = 0; n < NS; ++n)
-                h[n] = fmaf(exp2_hw(sum * a[n]), h[n], p.range_state[(int64_t)k * slot + at + n]);
+            for (int q = 0; q < U; ++q) {
+                const int k = min(k0 + q, r - 1);
+                sum[q] = su[(int64_t)k * p.batch * p.channels];
+#pragma unroll
+                for (int n = 0; n < NS; ++n) hr[q][n] = st[(int64_t)k * slot + n];
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q)
+                if (k0 + q < r)
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) h[n] = fmaf(exp2_hw(sum[q] * a[n]), h[n], hr[q][n]);
         }
     }
     const int64_t j = STATES ? p.seqlen : accepted(p, b);
@@ -165,6 +180,9 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
 #pragma unroll
         for (int n = 0; n < NS; ++n) p.state_out[at + n] = h[n];
 
+    // h and a have arrived: without this the compiler waits for every load in
+    // flight where the scan first uses them, in each tile.
+    wait_vmcnt<0>();
     double steps = 0.0;  // sum of the range's steps, rounded once at the end
     T *y = STATES ? nullptr : reinterpret_cast<T *>(p.y) + (b * p.seqlen + row) * p.channels + d0 + c8;
     for (int64_t t0 = t_lo; t0 < t_hi; t0 += kTile) {
@@ -175,12 +193,15 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
         {
             f32x4 dv[2], du[2];
 #pragma unroll
+            for (int i = 0; i < kCh; ++i) dv[i >> 2][i & 3] = rd.f32(i) + bias[i];
+            if (p.softplus) {
+#pragma unroll
+                for (int i = 0; i < kCh; ++i) dv[i >> 2][i & 3] = softplus(dv[i >> 2][i & 3]);
+            }
+#pragma unroll
             for (int i = 0; i < kCh; ++i) {
                 uv[i] = ru.f32(i);
-                float s = rd.f32(i) + bias[i];
-                if (p.softplus) s = softplus(s);
-                dv[i >> 2][i & 3] = s;
-                du[i >> 2][i & 3] = s * uv[i];
+                du[i >> 2][i & 3] = dv[i >> 2][i & 3] * uv[i];
             }
             *reinterpret_cast<f32x4 *>(&dls[row][c8]) = dv[0];
             *reinterpret_cast<f32x4 *>(&dls[row][c8 + 4]) = dv[1];
@@ -232,20 +253,22 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
         lds_barrier();
         if (!STATES && row < nt && nv > 0) {
             // Per (token, channel): the four partial sums, skip, gate, store.
-            Pack<T, kCh> o;
+            float f[kCh];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 f32x4 v = *reinterpret_cast<const f32x4 *>(&yps[0][row][c8 + 4 * q]);
 #pragma unroll
                 for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4 *>(&yps[w][row][c8 + 4 * q]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = 4 * q + i;
-                    float f = fmaf(skip[c], uv[c], v[i]);
-                    if (z) f *= silu(zc.f32(c));
-                    o.v[c] = from_f32<T>(f);
-                }
+                for (int i = 0; i < 4; ++i) f[4 * q + i] = fmaf(skip[4 * q + i], uv[4 * q + i], v[i]);
             }
+            if (gated) {
+#pragma unroll
+                for (int i = 0; i < kCh; ++i) f[i] *= silu(zc.f32(i));
+            }
+            Pack<T, kCh> o;
+#pragma unroll
+            for (int i = 0; i < kCh; ++i) o.v[i] = from_f32<T>(f[i]);
             T *yr = y + t0 * p.channels;
             if constexpr (ODD) {
 #pragma unroll
@@ -282,9 +305,36 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
+// Lane k of each quad, in all four of its lanes.
+template <int K>
+__device__ __forceinline__ float of_quad(float v) {
+    return dpp<K * 0x55>(v);
+}
+// v[k] summed over W = 4, 8 or 16 adjacent lanes, in the lanes at place k of
+// each quad.
+template <int W>
+__device__ __forceinline__ float lanes_sum4(const float (&v)[4]) {
+    const int q = threadIdx.x & 3;
+    // Halves, then quarters: each step keeps the values the lane's place asks
+    // for and hands the others over.
+    const float keep0 = q & 2 ? v[2] : v[0], give0 = q & 2 ? v[0] : v[2];
+    const float keep1 = q & 2 ? v[3] : v[1], give1 = q & 2 ? v[1] : v[3];
+    const float a = keep0 + dpp<0x4E>(give0), b = keep1 + dpp<0x4E>(give1);
+    float r = (q & 1 ? b : a) + dpp<0xB1>(q & 1 ? a : b);
+    if constexpr (W == 8) r += dpp<0x141>(dpp<0x1B>(r));  // the other quad: each reversed, then both mirrored
+    if constexpr (W == 16) {
+        r += dpp<0x124>(r);  // row_ror 4, then 8: all four quads of the row
+        r += dpp<0x128>(r);
+    }
+    return r;
+}
+
 // Few tokens: 4 states per lane, N/4 lanes per channel, so that the states are
-// read and written in whole 16-byte pieces, each once.
-template <typename T, int N>
+// read and written in whole 16-byte pieces, each once.  Four tokens go
+// together where there are as many (and the accepted index is not among
+// them): each lane of a quad does one token's softplus, gate and store, which
+// are the same for all states.
+template <typename T, int N, bool ONE>
 __global__ __launch_bounds__(kThreads) void scan_steps_kernel(SelectiveParams p) {
     constexpr int W = N / 4, CH = kThreads / W;
     const int tid = threadIdx.x, part = tid % W;
@@ -292,37 +342,76 @@ __global__ __launch_bounds__(kThreads) void scan_steps_kernel(SelectiveParams p)
     if (dg >= p.group_channels) return;  // whole groups of W lanes leave
     const int g = blockIdx.y, d = g * p.group_channels + dg;
     const int64_t b = blockIdx.z;
-    const T *u = reinterpret_cast<const T *>(p.u) + b * p.u_bs + d;
-    const T *dl = reinterpret_cast<const T *>(p.delta) + b * p.delta_bs + d;
-    const T *z = p.z ? reinterpret_cast<const T *>(p.z) + b * p.z_bs + d : nullptr;
-    const T *B = reinterpret_cast<const T *>(p.B) + b * p.B_bs + g * N + 4 * part;
-    const T *C = reinterpret_cast<const T *>(p.C) + b * p.C_bs + g * N + 4 * part;
-    T *y = reinterpret_cast<T *>(p.y) + b * p.seqlen * p.channels + d;
+    const int len = (int)p.seqlen;
+    // Token rows as uniform pointers plus a lane's own offset in them.
+    const T *u = reinterpret_cast<const T *>(p.u) + b * p.u_bs;
+    const T *dl = reinterpret_cast<const T *>(p.delta) + b * p.delta_bs;
+    const T *z = reinterpret_cast<const T *>(p.z) + (p.z ? b * p.z_bs : 0);
+    const T *B = reinterpret_cast<const T *>(p.B) + b * p.B_bs + g * N;
+    const T *C = reinterpret_cast<const T *>(p.C) + b * p.C_bs + g * N;
+    T *y = reinterpret_cast<T *>(p.y) + b * p.seqlen * p.channels;
     const int64_t at = (b * p.channels + d) * N + 4 * part;
     f32x4 h = {0.f, 0.f, 0.f, 0.f}, a = h;
     if (p.init_state) h = *reinterpret_cast<const f32x4 *>(p.init_state + at);
-    if (p.seqlen > 0) a = *reinterpret_cast<const f32x4 *>(p.A + (int64_t)d * N + 4 * part) * kLog2e;
+    if (len > 0) a = *reinterpret_cast<const f32x4 *>(p.A + (int64_t)d * N + 4 * part) * kLog2e;
     const float bias = p.delta_bias ? p.delta_bias[d] : 0.0f, skip = p.D ? p.D[d] : 0.0f;
-    const int64_t j = accepted(p, b);
+    const int j = (int)accepted(p, b);
     if (p.state_out && j < 0) *reinterpret_cast<f32x4 *>(p.state_out + at) = h;
-    for (int64_t t = 0; t < p.seqlen; ++t) {
-        const float uv = to_f32(u[t * p.u_ts]);
-        float s = to_f32(dl[t * p.delta_ts]) + bias;
-        const Pack<T, 4> bv = *reinterpret_cast<const Pack<T, 4> *>(B + t * p.B_ts);
-        const Pack<T, 4> cv = *reinterpret_cast<const Pack<T, 4> *>(C + t * p.C_ts);
-        const float zv = z ? to_f32(z[t * p.z_ts]) : 0.0f;
-        if (p.softplus) s = softplus(s);
-        const float du = s * uv;
+
+    auto advance = [&](float s, float du, const Pack<T, 4> &bv, const Pack<T, 4> &cv) {
         float acc = 0.0f;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             h[n] = fmaf(exp2_hw(s * a[n]), h[n], du * to_f32(bv.v[n]));
             acc = fmaf(h[n], to_f32(cv.v[n]), acc);
         }
+        return acc;
+    };
+    auto piece = [&](const T *row) { return *reinterpret_cast<const Pack<T, 4> *>(row + 4 * part); };
+    auto one = [&](int64_t t) {
+        const float uv = to_f32((u + t * p.u_ts)[d]);
+        float s = to_f32((dl + t * p.delta_ts)[d]) + bias;
+        const Pack<T, 4> bv = piece(B + t * p.B_ts), cv = piece(C + t * p.C_ts);
+        const float zv = p.z ? to_f32((z + t * p.z_ts)[d]) : 0.0f;
+        if (p.softplus) s = softplus(s);
+        float acc = advance(s, s * uv, bv, cv);
         acc = fmaf(skip, uv, lanes_sum<W>(acc));
-        if (z) acc *= silu(zv);
-        if (part == 0) y[t * p.channels] = from_f32<T>(acc);
+        if (p.z) acc *= silu(zv);
+        if (part == 0) (y + t * p.channels)[d] = from_f32<T>(acc);
         if (p.state_out && t == j) *reinterpret_cast<f32x4 *>(p.state_out + at) = h;
+    };
+    if constexpr (ONE) {
+        if (len > 0) one(0);
+    } else {
+        int t = 0;
+        if constexpr (W >= 4) {
+            const int q = tid & 3;
+            for (; t < len; t += 4) {
+                if (t + 4 > len || (j >= t && j < t + 4)) {
+                    for (int k = t; k < min(t + 4, len); ++k) one(k);
+                    continue;
+                }
+                const float uv = to_f32((u + (int64_t)(t + q) * p.u_ts)[d]);
+                float s = to_f32((dl + (int64_t)(t + q) * p.delta_ts)[d]) + bias;
+                const float zv = p.z ? to_f32((z + (int64_t)(t + q) * p.z_ts)[d]) : 0.0f;
+                Pack<T, 4> bv[4], cv[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    bv[k] = piece(B + (int64_t)(t + k) * p.B_ts);
+                    cv[k] = piece(C + (int64_t)(t + k) * p.C_ts);
+                }
+                if (p.softplus) s = softplus(s);
+                const float du = s * uv;
+                const float acc[4] = {advance(of_quad<0>(s), of_quad<0>(du), bv[0], cv[0]),
+                                      advance(of_quad<1>(s), of_quad<1>(du), bv[1], cv[1]),
+                                      advance(of_quad<2>(s), of_quad<2>(du), bv[2], cv[2]),
+                                      advance(of_quad<3>(s), of_quad<3>(du), bv[3], cv[3])};
+                float r = fmaf(skip, uv, lanes_sum4<W>(acc));
+                if (p.z) r *= silu(zv);
+                if (part < 4) (y + (int64_t)(t + q) * p.channels)[d] = from_f32<T>(r);
+            }
+        }
+        for (; t < len; ++t) one(t);
     }
     if (p.final_state) *reinterpret_cast<f32x4 *>(p.final_state + at) = h;
 }
@@ -349,7 +438,8 @@ hipError_t run(const SelectiveParams &p, hipStream_t stream) {
     if (p.seqlen <= kFewTokens) {
         constexpr int CH = kThreads / (N / 4);
         const dim3 grid((p.group_channels + CH - 1) / CH, p.ngroups, (unsigned)p.batch);
-        scan_steps_kernel<T, N><<<grid, kThreads, 0, stream>>>(p);
+        if (p.seqlen <= 1) scan_steps_kernel<T, N, true><<<grid, kThreads, 0, stream>>>(p);
+        else scan_steps_kernel<T, N, false><<<grid, kThreads, 0, stream>>>(p);
         return hipGetLastError();
     }
     return p.group_channels % kCh == 0 ? run_tiles<T, N, false>(p, stream) : run_tiles<T, N, true>(p, stream);
@@ -374,7 +464,7 @@ void selective_ranges(SelectiveParams &p) {
     // Workgroups of an unsplit call; the GPU holds three per compute unit.
     const int64_t tiles = (p.group_channels + kChannels - 1) / kChannels;
     const int64_t wgs = tiles * p.ngroups * p.batch;
-    constexpr int64_t kUnits = 256, kMinRange = 2 * kTile;
+    constexpr int64_t kUnits = 256, kMinRange = kTile;
     const int64_t want = std::min((3 * kUnits) / wgs, (p.seqlen + kMinRange - 1) / kMinRange);
     if (want < 4) return;
     p.range_len = ((p.seqlen + want - 1) / want + kTile - 1) / kTile * kTile;

@@ -147,6 +147,10 @@ SCAN = [
     ("one_token_odd_channels", 2, 1, 37, 16, 1, "bf16", True, True, True, True, True, 1),
     ("few_tokens_n64", 2, 7, 72, 64, 2, "bf16", True, True, True, True, True, 8),
     ("sixteen_n32", 2, 16, 200, 32, 1, "f32", True, True, True, True, True, 0),
+    ("few_n16_groups", 3, 13, 72, 16, 2, "bf16", True, True, True, True, True, 8),
+    ("few_n16_f32", 2, 8, 37, 16, 1, "f32", False, True, False, False, False, 3),
+    ("few_n8", 2, 11, 40, 8, 1, "bf16", True, True, True, True, True, 0),
+    ("few_n64_plain", 1, 15, 33, 64, 1, "f32", True, False, True, True, False, 0),
     ("seventeen", 2, 17, 136, 16, 2, "bf16", True, True, True, False, True, 8),
     ("tile_edges", 2, 65, 128, 16, 1, "bf16", True, True, True, True, True, 0),
     ("odd_everything", 3, 131, 75, 16, 3, "bf16", True, True, True, True, True, 5),
@@ -205,9 +209,9 @@ def test_scan(case):
         close("state_out", at, wa, ba)
 
 
-@pytest.mark.parametrize("j", [0, 15, 16, 31, 32, 63, 64, 299, 300])
-def test_scan_state_at_every_kind_of_index(j):
-    s = scan_inputs(gen(22), 1, 301, 64, 16, 1, "f32", True, False, True, True, 0)
+@pytest.mark.parametrize("T,j", [(301, j) for j in (0, 15, 16, 31, 32, 63, 64, 299, 300)] + [(10, j) for j in range(10)])
+def test_scan_state_at_every_kind_of_index(T, j):
+    s = scan_inputs(gen(22), 1, T, 64, 16, 1, "f32", True, False, True, True, 0)
     js = np.array([j], np.int32)
     y, fin, at = run_scan(s, True, torch.from_numpy(js).cuda())
     torch.cuda.synchronize()
