@@ -310,9 +310,10 @@ ssd_status ssd_state_correction(void *y, const float *dt, const float *A, const 
  * pointers, stream order, host-side checks before any launch, no allocation),
  * except that inputs named with a stride below need not be dense: strides are
  * in elements, >= 0 (0 repeats a row), and of no account along a dimension of
- * size 1 or less.  The innermost dimension is always contiguous.  Every
- * pointer is aligned to its own element; faster variants are taken where
- * pointers and strides allow 16-byte accesses.
+ * size 1 or less.  The innermost dimension is always contiguous.  Pointers
+ * need the alignment of one element unless said otherwise, and any strides and
+ * sizes within the limits are taken.  hip_stream belongs to the current device.
+ * These entry points were added to ABI version 8; nothing in it changed.
  * -------------------------------------------------------------------------*/
 
 /* Sizes of ssd_causal_conv_fwd.  batch and seqlen may be 0. */
@@ -436,7 +437,7 @@ typedef struct {
  *   z       [b,T,dim]  dtype  strided; NULL = no gate
  *   weight  [dim]      fp32   NULL = ones
  *   out     [b,T,dim]  dtype  dense; may be x or z itself where that is dense
- *   eps     >= 0 and finite
+ *   eps     >= 0 and finite (with 0 a part of zeros gives NaN)
  * One kernel, no workspace.  dim <= 2^20, b*T < 2^31. */
 ssd_status ssd_gated_norm_fwd(const void *x, const void *z, const float *weight, void *out,
                               float eps, int norm_before_gate,

@@ -461,11 +461,14 @@ void selective_ranges(SelectiveParams &p) {
     p.ranges = 1;
     p.range_len = (p.seqlen + kTile - 1) / kTile * kTile;
     if (p.seqlen <= kFewTokens || p.batch == 0) return;
-    // Workgroups of an unsplit call; the GPU holds three per compute unit.
+    // Workgroups of an unsplit call; a compute unit holds three (two with 32
+    // or more states, by registers).  Ranges double the work (us without /
+    // with them: 24 workgroups, 4093 tokens 438 / 65; 80, 2048 tokens 223 /
+    // 115; 160, 2048 tokens 228 / 190 with four ranges, 278 with two; 320,
+    // 2048 tokens 304 / 348 with two), hence at least four of them.
     const int64_t tiles = (p.group_channels + kChannels - 1) / kChannels;
-    const int64_t wgs = tiles * p.ngroups * p.batch;
-    constexpr int64_t kUnits = 256, kMinRange = kTile;
-    const int64_t want = std::min((3 * kUnits) / wgs, (p.seqlen + kMinRange - 1) / kMinRange);
+    const int64_t wgs = tiles * p.ngroups * p.batch, held = (p.dstate >= 32 ? 2 : 3) * (int64_t)256;
+    const int64_t want = std::min(held / wgs, (p.seqlen + kTile - 1) / kTile);
     if (want < 4) return;
     p.range_len = ((p.seqlen + want - 1) / want + kTile - 1) / kTile * kTile;
     p.ranges = (int)((p.seqlen + p.range_len - 1) / p.range_len);

@@ -110,6 +110,18 @@ def test_conv_steps_in_place_equal_one_call():
     assert torch.equal(got, want) and torch.equal(held, wfin)
 
 
+def test_conv_broadcast_rows():
+    # One row for all tokens, one sequence for all (strides of 0).
+    g = gen(5)
+    x = rnd(g, (1, 1, 40), "bf16").expand(2, 19, 40)
+    w, bias = rnd(g, (40, 3)), rnd(g, (40,))
+    o, fin, _ = ssd.ssd_causal_conv_fwd(x, w, bias)
+    torch.cuda.synchronize()
+    want, bound, wfin, _ = ref.conv(f64(x), f64(w), f64(bias), None, None, True, "bf16")
+    close("out", o, want, bound)
+    assert np.array_equal(f64(fin), wfin)
+
+
 def test_conv_empty_calls():
     w = torch.zeros(16, 4, device="cuda")
     init = torch.randn(2, 3, 16, device="cuda")
@@ -296,6 +308,19 @@ def test_scan_extreme_steps():
     close("final_state", fin, wf, bf)
 
 
+@pytest.mark.parametrize("b,Dm,T", [(12, 4096, 40), (1, 64, 4000), (3, 520, 333)])
+def test_scan_many_workgroups_and_many_ranges(b, Dm, T):
+    # More workgroups than the GPU holds at once; ranges of one and more tiles.
+    s = scan_inputs(gen(29), b, T, Dm, 8, 1, "bf16", True, True, True, True, 0)
+    js = np.array([(T - 1, T // 3, -1)[i % 3] for i in range(b)], np.int32)
+    y, fin, at = run_scan(s, True, torch.from_numpy(js).cuda())
+    torch.cuda.synchronize()
+    wy, by, wf, bf, wa, ba = ref_scan(s, True, js, "bf16")
+    close("y", y, wy, by)
+    close("final_state", fin, wf, bf)
+    close("state_out", at, wa, ba)
+
+
 def test_scan_broadcast_inputs():
     # One row of steps for all tokens and sequences (strides of 0).
     b, T, Dm, N = 3, 50, 64, 16
@@ -403,6 +428,8 @@ VERIFY = [
     ("many_drafts", 3, 70, 64, "f32", True, True),
     ("big_batch", 600, 2, 300, "f32", True, True),
     ("big_batch_wide", 300, 1, 20011, "f32", True, False),
+    ("rows_of_two_turns", 70, 1, 40009, "f32", True, True),     # a wave's piece passes 4096 elements
+    ("split_odd", 3, 2, 30011, "bf16", False, False),
 ]
 
 
