@@ -104,8 +104,9 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     float bias[kCh], skip[kCh];
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
-        bias[i] = p.delta_bias && i < nv ? p.delta_bias[d0 + c8 + i] : 0.0f;
-        skip[i] = !STATES && p.D && i < nv ? p.D[d0 + c8 + i] : 0.0f;
+        const int c = from + (ODD ? min(i, nread - 1) : i);
+        bias[i] = p.delta_bias ? p.delta_bias[c] : 0.0f;
+        skip[i] = !STATES && p.D ? p.D[c] : 0.0f;
     }
 
     // A tile's loads, none of them conditional so that they stay in flight.
@@ -137,28 +138,31 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     };
     load_tile(t_lo);
 
-    // Entering state of this lane's channel and quarter of the states.
+    // Entering state of this lane's channel and quarter of the states.  Lanes
+    // past the tile's channels carry its last one along and store nothing.
     const bool mine = lane < nch;
-    const int64_t dn = (int64_t)(d0 + lane) * N + wave * NS;     // into [D,N]
+    const int d = d0 + min(lane, nch - 1);
+    const int64_t dn = (int64_t)d * N + wave * NS;               // into [D,N]
     const int64_t at = b * p.channels * N + dn;                  // into [b,D,N]
     const int64_t slot = p.batch * p.channels * N;               // one range's states in the workspace
     float a[NS], h[NS];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) a[n] = mine ? p.A[dn + n] * kLog2e : 0.0f;
-    {
+    for (int n = 0; n < NS; ++n) a[n] = p.A[dn + n] * kLog2e;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) h[n] = 0.0f;
+    if (p.init_state && r == 0) {
         // Range 0 of the full pass takes init_state from the first launch's
         // copy: the last range may be writing final_state over it by now.
         const float *first = !STATES && p.ranges > 1 ? p.range_state + (int64_t)(p.ranges - 1) * slot : p.init_state;
 #pragma unroll
-        for (int n = 0; n < NS; ++n) h[n] = mine && p.init_state && r == 0 ? first[at + n] : 0.0f;
-    }
-    if (STATES) {
-        if (r == 0 && p.init_state && mine)
+        for (int n = 0; n < NS; ++n) h[n] = first[at + n];
+        if (STATES && mine)
 #pragma unroll
             for (int n = 0; n < NS; ++n) p.range_state[(int64_t)(p.ranges - 1) * slot + at + n] = h[n];
-    } else if (r > 0 && mine) {
+    }
+    if (!STATES && r > 0) {
         constexpr int U = NS > 8 ? 4 : 8;  // ranges whose loads are in flight together
-        const float *st = p.range_state + at, *su = p.range_steps + b * p.channels + d0 + lane;
+        const float *st = p.range_state + at, *su = p.range_steps + b * p.channels + d;
         for (int k0 = 0; k0 < r; k0 += U) {
             float sum[U], hr[U][NS];
 #pragma unroll
@@ -183,7 +187,7 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     // h and a have arrived: without this the compiler waits for every load in
     // flight where the scan first uses them, in each tile.
     wait_vmcnt<0>();
-    double steps = 0.0;  // sum of the range's steps, rounded once at the end
+    double steps = 0.0;  // sum of the range's steps (this wave's part), rounded once at the end
     T *y = STATES ? nullptr : reinterpret_cast<T *>(p.y) + (b * p.seqlen + row) * p.channels + d0 + c8;
     for (int64_t t0 = t_lo; t0 < t_hi; t0 += kTile) {
         const int nt = (int)min((int64_t)kTile, t_hi - t0);
@@ -230,11 +234,7 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
                 h[n] = fmaf(exp2_hw(s * a[n]), h[n], du * bc[n]);
                 if (!STATES) acc = n == 0 ? h[n] * bc[N] : fmaf(h[n], bc[N + n], acc);
             }
-            if (STATES) {
-                if (wave == 0) steps += (double)s;
-            } else {
-                yps[wave][t][lane] = acc;
-            }
+            if (!STATES) yps[wave][t][lane] = acc;
         };
         const bool here = !STATES && p.state_out && j >= t0 && j < t0 + nt;
         int t = 0;
@@ -249,6 +249,13 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
             if (part == 0 && mine)
 #pragma unroll
                 for (int n = 0; n < NS; ++n) p.state_out[at + n] = h[n];
+        }
+        if (STATES) {
+            // The sum of steps, a quarter of the tokens per wave.
+            constexpr int PART = kTile / kWaves;
+#pragma unroll
+            for (int k = 0; k < PART; ++k)
+                if (wave * PART + k < nt) steps += (double)dls[wave * PART + k][lane];
         }
         lds_barrier();
         if (!STATES && row < nt && nv > 0) {
@@ -279,11 +286,20 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
             }
         }
     }
+    if (STATES) {
+        // The waves' parts meet in LDS (its last readers are past a barrier).
+        double *parts = reinterpret_cast<double *>(&dls[0][0]);
+        parts[wave * 64 + lane] = steps;
+        lds_barrier();
+        if (wave == 0 && mine) {
+            for (int w = 1; w < kWaves; ++w) steps += parts[w * 64 + lane];
+            p.range_steps[((int64_t)r * p.batch + b) * p.channels + d] = (float)steps;
+        }
+    }
     if (!mine) return;
     if (STATES) {
 #pragma unroll
         for (int n = 0; n < NS; ++n) p.range_state[(int64_t)r * slot + at + n] = h[n];
-        if (wave == 0) p.range_steps[((int64_t)r * p.batch + b) * p.channels + d0 + lane] = (float)steps;
     } else if (p.final_state && t_hi == p.seqlen) {
 #pragma unroll
         for (int n = 0; n < NS; ++n) p.final_state[at + n] = h[n];
