@@ -25,7 +25,13 @@ __all__ = [
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libssd.so")
+_FAST_PATH = os.path.join(_PKG, "_fastcall.so")
 _lib = None
+# The short way of the operators around the scan for calls that fit as they
+# are (csrc/fastcall.cpp): the same checks, allocations and C call without
+# Python's share of their time.  It returns None for any other call, which the
+# code here then makes or refuses.
+_fast = None
 
 SSD_DTYPE_F32 = 0
 SSD_DTYPE_BF16 = 1
@@ -87,7 +93,7 @@ def library_path() -> str:
 
 
 def _load():
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     if not os.path.exists(_LIB_PATH):
@@ -137,6 +143,17 @@ def _load():
     lib.ssd_last_error.restype = ctypes.c_char_p
     lib.ssd_abi_version.argtypes = []
     lib.ssd_abi_version.restype = i32
+    if os.path.exists(_FAST_PATH):
+        import importlib.util
+
+        spec = importlib.util.spec_from_file_location(__name__ + "._fastcall", _FAST_PATH)
+        fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(fast)
+        fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.ssd_causal_conv_fwd, lib.ssd_selective_scan_fwd, lib.ssd_selective_scan_workspace_bytes,
+            lib.ssd_gated_norm_fwd, lib.ssd_verify_drafts, lib.ssd_verify_workspace_bytes)))
+        fast.raw_stream = torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None
+        _fast = fast
     _lib = lib
     return lib
 
@@ -434,6 +451,14 @@ def ssd_causal_conv_fwd(x, weight, bias=None, init_state=None, state_out_idx=Non
     (out, final_state or None, state_out or None); out is a tuple with
     `split`.  Errors as for ssd_chunk_scan_fwd.
     """
+    if _fast is not None and x.is_cuda and stream is None and out is None and state_out is None and (
+            activation == "silu" or activation is None):
+        r = _fast.conv(x, weight, bias, init_state, state_out_idx, split, activation is not None, final_state,
+                       return_final_state, _fast.raw_stream(x.device.index))
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(r)
     import torch
 
     if x.dim() != 3 or weight.dim() != 2:
@@ -511,6 +536,13 @@ def ssd_selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, i
     (y, final_state or None, state_out or None).  Errors as for
     ssd_chunk_scan_fwd.
     """
+    if _fast is not None and u.is_cuda and stream is None and y is None and state_out is None and workspace is None:
+        r = _fast.scan(u, delta, A, B, C, D, z, delta_bias, init_state, state_out_idx, delta_softplus, final_state,
+                       return_final_state, _fast.raw_stream(u.device.index))
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(r)
     import torch
 
     if u.dim() != 3 or A.dim() != 2 or B.dim() != 4:
@@ -598,6 +630,12 @@ def ssd_gated_norm_fwd(x, z=None, weight=None, *, ngroups: int = 1, eps: float =
     z itself where that is dense) is allocated when not given, and returned.
     Errors as for ssd_chunk_scan_fwd.
     """
+    if _fast is not None and x.is_cuda and stream is None and out is None:
+        r = _fast.norm(x, z, weight, ngroups, eps, norm_before_gate, _fast.raw_stream(x.device.index))
+        if r.__class__ is int:
+            _check(r)
+        if r is not None:
+            return r
     import torch
 
     if x.dim() < 1:
@@ -648,6 +686,14 @@ def ssd_verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, dr
     also the state_out_idx of a scan over [last token, drafts].  Errors as for
     ssd_chunk_scan_fwd.
     """
+    if _fast is not None and target_probs.is_cuda and stream is None and n_accepted is None and next_token is None \
+            and tokens is None and workspace is None:
+        r = _fast.verify(target_probs, draft_tokens, uniforms, draft_probs, draft_lens,
+                         _fast.raw_stream(target_probs.device.index))
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(r)
     import torch
 
     if target_probs.dim() != 3 or target_probs.shape[1] < 1:

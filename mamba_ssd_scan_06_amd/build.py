@@ -3,8 +3,9 @@
 Usage: python -m mamba_ssd_scan_06_amd.build   (or build() from Python)
 
 Each .hip file under csrc/ is compiled to an object in parallel, then the
-objects are linked into mamba_ssd_scan_06_amd/libssd.so.  Every build
-recompiles from source.
+objects are linked into mamba_ssd_scan_06_amd/libssd.so; csrc/fastcall.cpp
+(the Python binding's short way, host code against torch's headers) becomes
+mamba_ssd_scan_06_amd/_fastcall.so.  Every build recompiles from source.
 """
 from __future__ import annotations
 
@@ -19,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssd.so")
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [
@@ -52,6 +54,26 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
 
 
+def build_fastcall() -> str:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    tmp = FASTCALL + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.cpp"), "-o", tmp,
+           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building {FASTCALL} failed:\n{r.stderr}")
+    os.replace(tmp, FASTCALL)
+    return FASTCALL
+
+
 def build(jobs: int = 8, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = hipcc()
@@ -67,7 +89,9 @@ def build(jobs: int = 8, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        fast = ex.submit(build_fastcall)
         objs = list(ex.map(compile_one, sources()))
+        fast.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([cc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp],
                        capture_output=True, text=True)

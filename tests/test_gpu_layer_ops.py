@@ -648,3 +648,72 @@ def test_on_a_given_stream(T):
     got = ssd.ssd_gated_norm_fwd(*nrm, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(got, want[6])
+
+
+@pytest.mark.parametrize("T", [1, 45, 1200])
+def test_short_and_long_way_through_the_binding(T, monkeypatch):
+    s, c, nrm, ver = layer_inputs(91, T)
+    layer_run(s, c, nrm, ver)
+    assert ssd._fast is not None
+
+    def calls():
+        init = s["init"].clone()
+        out = list(run_scan(dict(s, init=init), True, None, final_state=init))          # in place, no index
+        held = c[3].clone()
+        out += list(ssd.ssd_causal_conv_fwd(c[0], c[1], None, held, split=(40, 32), activation=None, final_state=held)[0])
+        out += [held]
+        out += [ssd.ssd_causal_conv_fwd(c[0], c[1], return_final_state=False)[1]]
+        out += [run_scan(s, 1, return_final_state=0)[1]]                                  # truth values of other types
+        out += [ssd.ssd_gated_norm_fwd(nrm[0].view(2, T, -1), None, None, eps=0, norm_before_gate=True)]
+        out += [ssd.ssd_gated_norm_fwd(*nrm, ngroups=8, norm_before_gate=True)]
+        out += list(ssd.ssd_verify_drafts(ver[0], ver[1], ver[2], None, torch.tensor([1, 3], dtype=torch.int32).cuda()))
+        return layer_run(s, c, nrm, ver) + out
+
+    short = calls()
+    monkeypatch.setattr(ssd, "_fast", None)
+    long_ = calls()
+    torch.cuda.synchronize()
+    assert len(short) == len(long_)
+    for k, (a, b) in enumerate(zip(short, long_)):
+        assert (a is None and b is None) or (a.dtype == b.dtype and torch.equal(a, b)), k
+
+
+def test_refusals_on_the_gpu():
+    """Calls on GPU tensors that do not fit are refused whichever way they take."""
+    s, c, nrm, ver = layer_inputs(92, 5)
+    layer_run(s, c, nrm, ver)
+    x, w, bias, init, idx = c
+    bad = [
+        (TypeError, lambda: ssd.ssd_causal_conv_fwd(x, w.bfloat16(), bias)),
+        (ValueError, lambda: ssd.ssd_causal_conv_fwd(x, w[:-1], bias)),
+        (ValueError, lambda: ssd.ssd_causal_conv_fwd(x, w, bias, init[:, :2])),
+        (ValueError, lambda: ssd.ssd_causal_conv_fwd(x, w, bias, split=[72, 8])),
+        (ValueError, lambda: ssd.ssd_causal_conv_fwd(x, w, bias, split=[-8, 80])),
+        (ValueError, lambda: ssd.ssd_causal_conv_fwd(x, w, bias, activation="gelu")),
+        (ValueError, lambda: ssd.ssd_causal_conv_fwd(x, w.cpu(), bias)),
+        (TypeError, lambda: ssd.ssd_causal_conv_fwd(x.half(), w, bias)),
+        (ValueError, lambda: ssd.ssd_causal_conv_fwd(x, w, bias, init, final_state=init[:1])),
+        (TypeError, lambda: ssd.ssd_causal_conv_fwd(x, w, bias, init, idx.long())),
+        (ssd.SsdError, lambda: ssd.ssd_causal_conv_fwd(x, w, bias, final_state=x[:, :3].contiguous()[:, :3], out=x)),
+        (ssd.SsdError, lambda: ssd.ssd_causal_conv_fwd(x, torch.zeros(72, 5, device="cuda"))),
+        (ValueError, lambda: run_scan(dict(s, B=s["B"].transpose(1, 3).contiguous().transpose(1, 3)), True)),
+        (TypeError, lambda: run_scan(dict(s, A=s["A"].double()), True)),
+        (ValueError, lambda: run_scan(dict(s, z=s["z"][:, :4]), True)),
+        (ssd.SsdError, lambda: run_scan(dict(s, A=s["A"][:, :4].contiguous(), B=s["B"][..., :4].contiguous(),
+                                             C=s["C"][..., :4].contiguous(), init=None), True)),
+        (ssd.SsdError, lambda: run_scan(s, True, final_state=s["init"].view(-1)[:2 * 72 * 16].view(2, 72, 16),
+                                        y=s["init"].view(torch.bfloat16).view(-1)[:2 * 5 * 72].view(2, 5, 72))),
+        (ValueError, lambda: ssd.ssd_gated_norm_fwd(nrm[0], nrm[1][:-1], nrm[2])),
+        (TypeError, lambda: ssd.ssd_gated_norm_fwd(nrm[0], nrm[1].float(), nrm[2])),
+        (ssd.SsdError, lambda: ssd.ssd_gated_norm_fwd(*nrm, ngroups=5)),
+        (ssd.SsdError, lambda: ssd.ssd_gated_norm_fwd(*nrm, ngroups=-1)),
+        (ssd.SsdError, lambda: ssd.ssd_gated_norm_fwd(*nrm, eps=-1.0)),
+        (ValueError, lambda: ssd.ssd_verify_drafts(ver[0], ver[1][:, :3], ver[2], ver[3])),
+        (TypeError, lambda: ssd.ssd_verify_drafts(ver[0], ver[1].long(), ver[2], ver[3])),
+        (TypeError, lambda: ssd.ssd_verify_drafts(ver[0], ver[1], ver[2], ver[3].bfloat16())),
+        (ValueError, lambda: ssd.ssd_verify_drafts(ver[0], ver[1], ver[2].cpu(), ver[3])),
+    ]
+    for k, (kind, call) in enumerate(bad):
+        print("refusal", k, flush=True)
+        with pytest.raises(kind):
+            call()
