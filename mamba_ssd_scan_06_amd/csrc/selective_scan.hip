@@ -49,9 +49,10 @@ template <typename T>
 struct Row8 {
     static constexpr int W = sizeof(T) * 8 / 16, VEC = 16 / sizeof(T);
     u32x4 v[W];
-    __device__ __forceinline__ void load(const T *p) {
+    // 16 bytes from each of the offsets.
+    __device__ __forceinline__ void load(const T *p, const int (&at)[W]) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) v[k] = load_words(p + k * VEC);
+        for (int k = 0; k < W; ++k) v[k] = load_words(p + at[k]);
     }
     // Element by element, the last of `valid` repeated.
     __device__ __forceinline__ void load(const T *p, int valid) {
@@ -72,7 +73,7 @@ __device__ __forceinline__ int64_t accepted(const SelectiveParams &p, int64_t b)
 }
 
 // STATES: leave the range's final state and sum of steps only.  ODD: a group's
-// channels are no multiple of 8, so that rows are read element by element.
+// channels are no multiple of 16 bytes, so that rows are read element by element.
 template <typename T, int N, bool STATES, bool ODD>
 __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p) {
     constexpr int NS = N / kWaves;        // states per lane
@@ -97,19 +98,23 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     // This thread's 8 channels of one token of a tile.
     const int row = tid >> 3, c8 = (tid & 7) * kCh;
     const int nv = max(0, min(kCh, nch - c8));
-    // Where they are read: pieces past the tile's channels read its last
-    // channels again, and nothing comes of them.
-    const int from = d0 + (ODD ? min(c8, nch - 1) : min(c8, nch - kCh)), nread = ODD ? max(nv, 1) : kCh;
-    const T *u = reinterpret_cast<const T *>(p.u) + b * p.u_bs + from;
-    const T *dl = reinterpret_cast<const T *>(p.delta) + b * p.delta_bs + from;
+    // Where they are read, in vectors of 16 bytes: those past the tile's
+    // channels read its last ones again, and nothing comes of them.
+    constexpr int VEC = Row8<T>::VEC, VECS = Row8<T>::W;
+    int off[VECS];
+#pragma unroll
+    for (int k = 0; k < VECS; ++k) off[k] = ODD ? min(c8, nch - 1) : min(c8 + k * VEC, nch - VEC);
+    const int nread = max(nv, 1);  // ODD: elements from off[0] on
+    const T *u = reinterpret_cast<const T *>(p.u) + b * p.u_bs + d0;
+    const T *dl = reinterpret_cast<const T *>(p.delta) + b * p.delta_bs + d0;
     const bool gated = !STATES && p.z != nullptr;
-    const T *z = reinterpret_cast<const T *>(p.z) + (gated ? b * p.z_bs + from : 0);
+    const T *z = reinterpret_cast<const T *>(p.z) + (gated ? b * p.z_bs + d0 : 0);
     const T *B = reinterpret_cast<const T *>(p.B) + b * p.B_bs + g * N;
     const T *C = reinterpret_cast<const T *>(p.C) + b * p.C_bs + g * N;
     float bias[kCh], skip[kCh];
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
-        const int c = from + (ODD ? min(i, nread - 1) : i);
+        const int c = d0 + (ODD ? off[0] + min(i, nread - 1) : off[i / VEC] + i % VEC);
         bias[i] = p.delta_bias ? p.delta_bias[c] : 0.0f;
         skip[i] = !STATES && p.D ? p.D[c] : 0.0f;
     }
@@ -125,13 +130,13 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
         const T *pu = u + t0 * p.u_ts + tr * p.u_ts, *pd = dl + t0 * p.delta_ts + tr * p.delta_ts,
                 *pz = z + t0 * p.z_ts + tr * p.z_ts;
         if constexpr (ODD) {
-            ru.load(pu, nread);
-            rd.load(pd, nread);
-            if (gated) rz.load(pz, nread);
+            ru.load(pu + off[0], nread);
+            rd.load(pd + off[0], nread);
+            if (gated) rz.load(pz + off[0], nread);
         } else {
-            ru.load(pu);
-            rd.load(pd);
-            if (gated) rz.load(pz);
+            ru.load(pu, off);
+            rd.load(pd, off);
+            if (gated) rz.load(pz, off);
         }
         const T *Bt = B + t0 * p.B_ts, *Ct = C + t0 * p.C_ts;
 #pragma unroll
@@ -278,16 +283,19 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
 #pragma unroll
                 for (int i = 0; i < kCh; ++i) f[i] *= silu(zc.f32(i));
             }
-            Pack<T, kCh> o;
-#pragma unroll
-            for (int i = 0; i < kCh; ++i) o.v[i] = from_f32<T>(f[i]);
             T *yr = y + t0 * p.channels;
             if constexpr (ODD) {
 #pragma unroll
                 for (int i = 0; i < kCh; ++i)
-                    if (i < nv) yr[i] = o.v[i];
+                    if (i < nv) yr[i] = from_f32<T>(f[i]);
             } else {
-                *reinterpret_cast<Pack<T, kCh> *>(yr) = o;
+#pragma unroll
+                for (int k = 0; k < VECS; ++k) {
+                    float part[VEC];
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) part[i] = f[k * VEC + i];
+                    if (k * VEC < nv) store_words(yr + k * VEC, to_words(part, T()));
+                }
             }
         }
     }
@@ -465,7 +473,7 @@ hipError_t run(const SelectiveParams &p, hipStream_t stream) {
         else scan_steps_kernel<T, N, false><<<grid, kThreads, 0, stream>>>(p);
         return hipGetLastError();
     }
-    return p.group_channels % kCh == 0 ? run_tiles<T, N, false>(p, stream) : run_tiles<T, N, true>(p, stream);
+    return p.group_channels % (int)(16 / sizeof(T)) == 0 ? run_tiles<T, N, false>(p, stream) : run_tiles<T, N, true>(p, stream);
 }
 
 template <typename T>

@@ -167,6 +167,8 @@ SCAN = [
     ("tile_edges", 2, 65, 128, 16, 1, "bf16", True, True, True, True, True, 0),
     ("odd_everything", 3, 131, 75, 16, 3, "bf16", True, True, True, True, True, 5),
     ("f32_odd", 2, 101, 33, 8, 1, "f32", True, True, True, True, True, 3),
+    ("f32_fours", 2, 70, 2 * 500, 64, 2, "f32", False, False, True, True, True, 1),
+    ("f32_four_channels", 3, 60, 12, 16, 3, "f32", True, True, True, True, True, 0),
     ("no_extras", 1, 150, 64, 16, 1, "bf16", False, False, False, False, False, 0),
     ("n64_groups", 2, 90, 160, 64, 4, "f32", False, True, True, True, True, 4),
     ("long_few", 1, 1501, 72, 16, 1, "bf16", True, True, True, True, True, 8),
