@@ -652,6 +652,25 @@ def test_on_a_given_stream(T):
     assert torch.equal(got, want[6])
 
 
+@pytest.mark.parametrize("T", [5, 1200])
+def test_two_streams_at_once(T):
+    """Calls that may overlap on two streams, each with its own workspace."""
+    ins = [layer_inputs(k, T) for k in (74, 75)]
+    want = [[t.clone() for t in layer_run(*i)] for i in ins]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for turn in range(4):
+        for k in (0, 1):
+            with torch.cuda.stream(side[k]):
+                got[k].append(layer_run(*ins[k]))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for turn, outs in enumerate(got[k]):
+            for i, (a, b) in enumerate(zip(outs, want[k])):
+                assert torch.equal(a, b), (k, turn, i)
+
+
 @pytest.mark.parametrize("T", [1, 45, 1200])
 def test_short_and_long_way_through_the_binding(T, monkeypatch):
     s, c, nrm, ver = layer_inputs(91, T)
