@@ -61,6 +61,9 @@ CONV = [
     ("even_start", 2, 40, [64, 8, 8], 4, "bf16", True, True, True, True, 2, 4),
     ("f32_odd", 2, 131, [129, 7], 2, "f32", True, True, True, True, 1, 0),
     ("f32_wide", 1, 70, [1032, 16, 16], 4, "f32", True, True, False, False, 0, 0),
+    ("tiny_outputs", 2, 21, [3, 2, 5], 4, "bf16", True, True, True, True, 1, 3),
+    ("tiny_then_wide", 2, 21, [3, 70, 1], 3, "f32", True, True, True, True, 0, 0),
+    ("one_channel", 2, 12, [1], 2, "bf16", False, True, True, True, 0, 1),
     ("layer_2_7b", 2, 100, [5120, 128, 128], 4, "bf16", True, True, False, True, 5120, 80),
 ]
 
@@ -89,10 +92,11 @@ def test_conv(case):
         assert np.array_equal(f64(at), wat)
 
 
-def test_conv_steps_in_place_equal_one_call():
+@pytest.mark.parametrize("ch", [48, 53, 5, 2051])
+def test_conv_steps_in_place_equal_one_call(ch):
     # Token by token with the state updated in place gives the whole call's bits.
     g = gen(3)
-    b, T, ch = 3, 9, 48
+    b, T = 3, 9
     x, w, bias = rnd(g, (b, T, ch), "bf16"), rnd(g, (ch, 4)), rnd(g, (ch,))
     state = rnd(g, (b, 3, ch), "bf16").contiguous()
     whole, fin, _ = ssd.ssd_causal_conv_fwd(x, w, bias, state)
