@@ -82,19 +82,16 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, unsigned run, int 
     // the time they store: final_state may be the same memory.
     if (run == 0 && (p.state_out || p.final_state)) {
         u32x4 at[W - 1], fin[W - 1];
-        auto inputs = [&](u32x4 (&v)[W - 1], int64_t last) {  // the W-1 inputs ending at token `last`
+        // The W-1 inputs ending at token `last`, the first `before` of them held
+        // from before token 0 (uniform conditions, constant indices).
+        auto inputs = [&](u32x4 (&v)[W - 1], int64_t last) {
+            const int before = (int)max((int64_t)(W - 2) - last, (int64_t)0);
+            static_for<W>([&](auto c) {
+                if (before != c) return;
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) {
-                const int64_t t = last - (W - 2) + k;  // >= -(W-1); a uniform condition
-                if (t >= 0) {
-                    v[k] = load(x + t * p.x_ts);
-                } else {
-                    v[k] = hist[0];
-#pragma unroll
-                    for (int m = 1; m < W - 1; ++m)
-                        if (t + (W - 1) == m) v[k] = hist[m];
-                }
-            }
+                for (int k = 0; k < W - 1; ++k)
+                    v[k] = k < c ? hist[(k + W - 1 - c) % (W - 1)] : load(x + (last - (W - 2) + k) * p.x_ts);
+            });
         };
         auto keep = [&](void *to, const u32x4 (&v)[W - 1]) {
 #pragma unroll
