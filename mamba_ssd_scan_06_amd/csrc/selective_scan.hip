@@ -497,14 +497,18 @@ void selective_ranges(SelectiveParams &p) {
     p.range_len = (p.seqlen + kTile - 1) / kTile * kTile;
     if (p.seqlen <= kFewTokens || p.batch == 0) return;
     // Workgroups of an unsplit call; a compute unit holds three (two with 32
-    // or more states, by registers).  Ranges double the work (us without /
-    // with them: 24 workgroups, 4093 tokens 438 / 65; 80, 2048 tokens 223 /
-    // 115; 160, 2048 tokens 228 / 190 with four ranges, 278 with two; 320,
-    // 2048 tokens 304 / 348 with two), hence at least four of them.
+    // or more states, by LDS and registers).  Ranges double the work and cost
+    // another launch and prologue, some 6 us: with one workgroup on a compute
+    // unit taking 0.109 us per token and three of them 0.209 (N 16), they pay
+    // from T (1 - wgs / 224) = 55 tokens on, fewer with more states.  (us
+    // without / with them: 24 workgroups, 200 tokens 27 / 16, 4093 tokens 438 /
+    // 61; 80, 100 tokens 15.5 / 13.8, 2048 tokens 223 / 115; 192, 100 tokens
+    // 16 / 22; 160, 2048 tokens 228 / 190 with four ranges, 278 with two; 320,
+    // 2048 tokens 304 / 348 with two: hence at least four.)
     const int64_t tiles = (p.group_channels + kChannels - 1) / kChannels;
     const int64_t wgs = tiles * p.ngroups * p.batch, held = (p.dstate >= 32 ? 2 : 3) * (int64_t)256;
     const int64_t want = std::min(held / wgs, (p.seqlen + kTile - 1) / kTile);
-    if (want < 4) return;
+    if (want < 4 || p.seqlen * (224 - wgs) * p.dstate < (int64_t)3 << 16) return;
     p.range_len = ((p.seqlen + want - 1) / want + kTile - 1) / kTile * kTile;
     p.ranges = (int)((p.seqlen + p.range_len - 1) / p.range_len);
 }
