@@ -28,7 +28,8 @@
 // init_state) without outputs and leaves its final state and the sum of its
 // steps; in the second launch each range forms its entering state,
 //     h <- exp(A sum_of_steps) h + range's final state,
-// over the ranges before it, and runs in full.  That doubles the work, so
+// over the ranges before it (scaled_by_exp2 where A or the steps let that
+// factor grow), and runs in full.  That doubles the work, so
 // ranges are used only where they at least quadruple the workgroups
 // (selective_ranges has the figures).
 #include "device_common.hpp"
@@ -70,6 +71,15 @@ __device__ __forceinline__ int64_t accepted(const SelectiveParams &p, int64_t b)
     if (!p.state_out) return p.seqlen;
     const int64_t j = p.state_out_idx[b];
     return j < -1 ? -1 : (j > p.seqlen - 1 ? p.seqlen - 1 : j);
+}
+
+// h 2^x for any x: the power's whole part goes into h's exponent, so that it
+// overflows or vanishes only where the product does (0 stays 0; beyond 2^300
+// either way nothing of fp32 is left).
+__device__ __forceinline__ float scaled_by_exp2(float h, float x) {
+    x = fminf(fmaxf(x, -300.0f), 300.0f);
+    const float whole = ceilf(x);
+    return ldexpf(h * exp2_hw(x - whole), (int)whole);
 }
 
 // STATES: leave the range's final state and sum of steps only.  ODD: a group's
@@ -173,6 +183,9 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
     if (!STATES && r > 0) {
         constexpr int U = NS > 8 ? 4 : 8;  // ranges whose loads are in flight together
         const float *st = p.range_state + at, *su = p.range_steps + b * p.channels + d;
+        float a_most = a[0];
+#pragma unroll
+        for (int n = 1; n < NS; ++n) a_most = fmaxf(a_most, a[n]);
         for (int k0 = 0; k0 < r; k0 += U) {
             float sum[U], hr[U][NS];
 #pragma unroll
@@ -182,11 +195,26 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
 #pragma unroll
                 for (int n = 0; n < NS; ++n) hr[q][n] = st[(int64_t)k * slot + n];
             }
+            float sum_least = sum[0];
 #pragma unroll
-            for (int q = 0; q < U; ++q)
-                if (k0 + q < r)
+            for (int q = 1; q < U; ++q) sum_least = fminf(sum_least, sum[q]);
+            // A decay that may grow (A > 0, or steps < 0) takes another way,
+            // chosen by the wave: its factor over a whole range may pass the
+            // fp32 range where the state does not, and an empty state's 0
+            // times +inf would be NaN.
+            if (__builtin_expect(__any(a_most > 0.0f || sum_least < 0.0f), 0)) {
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) h[n] = fmaf(exp2_hw(sum[q] * a[n]), h[n], hr[q][n]);
+                for (int q = 0; q < U; ++q)
+                    if (k0 + q < r)
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) h[n] = scaled_by_exp2(h[n], sum[q] * a[n]) + hr[q][n];
+            } else {
+#pragma unroll
+                for (int q = 0; q < U; ++q)
+                    if (k0 + q < r)
+#pragma unroll
+                        for (int n = 0; n < NS; ++n) h[n] = fmaf(exp2_hw(sum[q] * a[n]), h[n], hr[q][n]);
+            }
         }
     }
     const int64_t j = STATES ? p.seqlen : accepted(p, b);
