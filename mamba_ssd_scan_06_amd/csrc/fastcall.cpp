@@ -76,6 +76,21 @@ PyObject *three(PyObject *a, PyObject *b, PyObject *c) {
 }
 void *stream_of(PyObject *o) { return PyLong_AsVoidPtr(o); }
 
+// Gives the interpreter lock away, as ctypes does around a foreign function: a
+// launch waits where the stream's queue is full and an allocation may wait for
+// the GPU, and other Python threads (one that the queue itself waits for among
+// them, in a host callback) run meanwhile.  Nothing of Python is touched while
+// it lives; it takes the lock back before an exception passes.
+class Unlocked {
+    PyThreadState *state_ = PyEval_SaveThread();
+
+public:
+    Unlocked() = default;
+    Unlocked(const Unlocked &) = delete;
+    Unlocked &operator=(const Unlocked &) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state_); }
+};
+
 // No C++ exception leaves a function called from Python: torch's macros turn
 // it into the Python error it stands for (out of memory among them).
 template <typename F>
@@ -121,17 +136,22 @@ PyObject *conv(PyObject *, PyObject *const *a, Py_ssize_t n) {
             !dense(init, {b, W - 1, ch}, type, dev) || !dense(idx, {b}, at::kInt, dev) ||
             !dense(fin, {b, W - 1, ch}, type, dev))
             return none();
-        const auto opt = x.t.options();
+        const bool want_final = a[8] == Py_True, silu = a[6] == Py_True;
+        void *const stream = stream_of(a[9]);
         at::Tensor out[3], at_j;
-        for (int i = 0; i < outs; ++i) out[i] = at::empty({b, T, sizes[i]}, opt);
-        if (!fin.t.defined() && a[8] == Py_True) fin.t = at::empty({b, W - 1, ch}, opt);
-        if (idx.t.defined()) at_j = at::empty({b, W - 1, ch}, opt);
-        ssd_conv_shape s = {b, T, {sizes[0], sizes[1], sizes[2]}, W, x.t.stride(0), x.t.stride(1)};
-        auto p = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
-        const ssd_status st =
-            g_conv(x.ptr(), (const float *)w.ptr(), (const float *)bias.ptr(), init.ptr(),
-                   a[6] == Py_True ? SSD_ACT_SILU : SSD_ACT_NONE, p(out[0]), p(out[1]), p(out[2]), fin.ptr(),
-                   (const int32_t *)idx.ptr(), p(at_j), &s, (ssd_dtype)code, stream_of(a[9]));
+        ssd_status st;
+        {
+            const Unlocked unlocked;
+            const auto opt = x.t.options();
+            for (int i = 0; i < outs; ++i) out[i] = at::empty({b, T, sizes[i]}, opt);
+            if (!fin.t.defined() && want_final) fin.t = at::empty({b, W - 1, ch}, opt);
+            if (idx.t.defined()) at_j = at::empty({b, W - 1, ch}, opt);
+            ssd_conv_shape s = {b, T, {sizes[0], sizes[1], sizes[2]}, W, x.t.stride(0), x.t.stride(1)};
+            auto p = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
+            st = g_conv(x.ptr(), (const float *)w.ptr(), (const float *)bias.ptr(), init.ptr(),
+                        silu ? SSD_ACT_SILU : SSD_ACT_NONE, p(out[0]), p(out[1]), p(out[2]), fin.ptr(),
+                        (const int32_t *)idx.ptr(), p(at_j), &s, (ssd_dtype)code, stream);
+        }
         if (st != SSD_OK) return PyLong_FromLong(st);
         PyObject *o;
         if (a[5] == Py_None) {
@@ -164,21 +184,25 @@ PyObject *scan(PyObject *, PyObject *const *a, Py_ssize_t n) {
             !dense(bias, {ch}, at::kFloat, dev) || !dense(init, {b, ch, N}, at::kFloat, dev) ||
             !dense(idx, {b}, at::kInt, dev) || !dense(fin, {b, ch, N}, at::kFloat, dev))
             return none();
-        auto st = [](const Arg &t, int d) { return t.t.defined() ? t.t.stride(d) : 0; };
-        ssd_selective_shape s = {b,        T,        ch,       N,        G,        st(u, 0), st(u, 1), st(dl, 0),
-                                 st(dl, 1), st(z, 0), st(z, 1), st(B, 0), st(B, 1), st(C, 0), st(C, 1)};
-        const size_t bytes = g_scan_bytes(&s, (ssd_dtype)code);
-        const at::Tensor y = at::empty({b, T, ch}, u.t.options());
-        at::Tensor at_j, ws;
-        if (!fin.t.defined() && a[12] == Py_True) fin.t = at::empty({b, ch, N}, A.t.options());
-        if (idx.t.defined()) at_j = at::empty({b, ch, N}, A.t.options());
-        if (bytes > 0) ws = at::empty({(int64_t)bytes}, A.t.options().dtype(at::kByte));
-        auto p = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
-        const ssd_status r =
-            g_scan(u.ptr(), dl.ptr(), (const float *)A.ptr(), B.ptr(), C.ptr(), (const float *)D.ptr(), z.ptr(),
-                   (const float *)bias.ptr(), a[10] == Py_True, (const float *)init.ptr(), y.data_ptr(),
-                   (float *)fin.ptr(), (const int32_t *)idx.ptr(), (float *)p(at_j), &s, (ssd_dtype)code, p(ws), bytes,
-                   stream_of(a[13]));
+        const bool want_final = a[12] == Py_True, softplus = a[10] == Py_True;
+        void *const stream = stream_of(a[13]);
+        at::Tensor y, at_j, ws;
+        ssd_status r;
+        {
+            const Unlocked unlocked;
+            auto st = [](const Arg &t, int d) { return t.t.defined() ? t.t.stride(d) : 0; };
+            ssd_selective_shape s = {b,        T,        ch,       N,        G,        st(u, 0), st(u, 1), st(dl, 0),
+                                     st(dl, 1), st(z, 0), st(z, 1), st(B, 0), st(B, 1), st(C, 0), st(C, 1)};
+            const size_t bytes = g_scan_bytes(&s, (ssd_dtype)code);
+            y = at::empty({b, T, ch}, u.t.options());
+            if (!fin.t.defined() && want_final) fin.t = at::empty({b, ch, N}, A.t.options());
+            if (idx.t.defined()) at_j = at::empty({b, ch, N}, A.t.options());
+            if (bytes > 0) ws = at::empty({(int64_t)bytes}, A.t.options().dtype(at::kByte));
+            auto p = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
+            r = g_scan(u.ptr(), dl.ptr(), (const float *)A.ptr(), B.ptr(), C.ptr(), (const float *)D.ptr(), z.ptr(),
+                       (const float *)bias.ptr(), softplus, (const float *)init.ptr(), y.data_ptr(), (float *)fin.ptr(),
+                       (const int32_t *)idx.ptr(), (float *)p(at_j), &s, (ssd_dtype)code, p(ws), bytes, stream);
+        }
         if (r != SSD_OK) return PyLong_FromLong(r);
         return three(wrap(y), wrap(fin.t), wrap(at_j));
     });
@@ -202,13 +226,20 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             PyErr_Clear();
             return none();
         }
-        const at::Tensor out = at::empty(x.t.sizes(), x.t.options());
-        auto bs = [&](const at::Tensor &t) { return !t.defined() || two ? 0 : t.stride(0); };
-        ssd_norm_shape s = {b,           T,       dim, groups, bs(x.t), x.t.stride(-2),
-                            bs(z.t), z.t.defined() ? z.t.stride(-2) : 0};
-        const ssd_status st = g_norm(x.ptr(), z.ptr(), (const float *)w.ptr(), out.data_ptr(),
-                                     (float)PyFloat_AS_DOUBLE(a[4]), a[5] == Py_True, &s, (ssd_dtype)code,
-                                     stream_of(a[6]));
+        const float eps = (float)PyFloat_AS_DOUBLE(a[4]);
+        const bool norm_first = a[5] == Py_True;
+        void *const stream = stream_of(a[6]);
+        at::Tensor out;
+        ssd_status st;
+        {
+            const Unlocked unlocked;
+            out = at::empty(x.t.sizes(), x.t.options());
+            auto bs = [&](const at::Tensor &t) { return !t.defined() || two ? 0 : t.stride(0); };
+            ssd_norm_shape s = {b,           T,       dim, groups, bs(x.t), x.t.stride(-2),
+                                bs(z.t), z.t.defined() ? z.t.stride(-2) : 0};
+            st = g_norm(x.ptr(), z.ptr(), (const float *)w.ptr(), out.data_ptr(), eps, norm_first, &s, (ssd_dtype)code,
+                        stream);
+        }
         return st != SSD_OK ? PyLong_FromLong(st) : wrap(out);
     });
 }
@@ -227,17 +258,24 @@ PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
             !dense(tok, {b, K}, at::kInt, dev, true) || !dense(u, {b, K + 1}, at::kFloat, dev, true) ||
             !dense(lens, {b}, at::kInt, dev))
             return none();
-        ssd_verify_shape s = {b, K, V, p.t.stride(0), p.t.stride(1), q.t.defined() ? q.t.stride(0) : 0,
-                              q.t.defined() ? q.t.stride(1) : 0};
-        const size_t bytes = g_verify_bytes(&s, (ssd_dtype)code);
-        const auto opt = tok.t.options();
-        const at::Tensor count = at::empty({b}, opt), next = at::empty({b}, opt), all = at::empty({b, K + 1}, opt);
-        at::Tensor ws;
-        if (bytes > 0) ws = at::empty({(int64_t)bytes}, opt.dtype(at::kByte));
-        const ssd_status st = g_verify(p.ptr(), q.ptr(), (const int32_t *)tok.ptr(), (const int32_t *)lens.ptr(),
-                                       (const float *)u.ptr(), (int32_t *)count.data_ptr(), (int32_t *)next.data_ptr(),
-                                       (int32_t *)all.data_ptr(), &s, (ssd_dtype)code,
-                                       ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(a[5]));
+        void *const stream = stream_of(a[5]);
+        at::Tensor count, next, all, ws;
+        ssd_status st;
+        {
+            const Unlocked unlocked;
+            ssd_verify_shape s = {b, K, V, p.t.stride(0), p.t.stride(1), q.t.defined() ? q.t.stride(0) : 0,
+                                  q.t.defined() ? q.t.stride(1) : 0};
+            const size_t bytes = g_verify_bytes(&s, (ssd_dtype)code);
+            const auto opt = tok.t.options();
+            count = at::empty({b}, opt);
+            next = at::empty({b}, opt);
+            all = at::empty({b, K + 1}, opt);
+            if (bytes > 0) ws = at::empty({(int64_t)bytes}, opt.dtype(at::kByte));
+            st = g_verify(p.ptr(), q.ptr(), (const int32_t *)tok.ptr(), (const int32_t *)lens.ptr(),
+                          (const float *)u.ptr(), (int32_t *)count.data_ptr(), (int32_t *)next.data_ptr(),
+                          (int32_t *)all.data_ptr(), &s, (ssd_dtype)code, ws.defined() ? ws.data_ptr() : nullptr, bytes,
+                          stream);
+        }
         if (st != SSD_OK) return PyLong_FromLong(st);
         return three(wrap(count), wrap(next), wrap(all));
     });
