@@ -124,7 +124,7 @@ __device__ __forceinline__ void conv_run(const ConvParams &p, unsigned run, int 
 #pragma unroll
             for (int k = 0; k + 1 < W - 1; ++k) last[k][i] = last[k + 1][i];
             last[W - 2][i] = cur;
-            r[i] = p.silu ? silu(acc) : acc;
+            r[i] = p.silu ? silu<T>(acc) : acc;
         }
         return to_words(r, T());
     };

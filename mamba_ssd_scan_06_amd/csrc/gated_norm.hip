@@ -60,7 +60,7 @@ __global__ __launch_bounds__(MAX) void gated_norm_kernel(NormParams p, NormGrid 
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 v[i] = word_f32(xr, i, T());
-                if (z && !p.norm_before_gate) v[i] *= silu(word_f32(zr, i, T()));
+                if (z && !p.norm_before_gate) v[i] *= silu<T>(word_f32(zr, i, T()));
             }
         };
         auto scaled = [&](const float (&v)[VEC], const u32x4 &zr, const u32x4 (&wv)[VEC / 4], float scale) {
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(MAX) void gated_norm_kernel(NormParams p, NormGrid 
             for (int i = 0; i < VEC; ++i) {
                 float f = v[i] * scale;
                 if (weight) f *= word_f32(wv[i / 4], i % 4, float());
-                if (z && p.norm_before_gate) f *= silu(word_f32(zr, i, T()));
+                if (z && p.norm_before_gate) f *= silu<T>(word_f32(zr, i, T()));
                 o[i] = f;
             }
             return to_words(o, T());

@@ -313,7 +313,7 @@ __global__ __launch_bounds__(kThreads) void scan_tiles_kernel(SelectiveParams p)
             }
             if (gated) {
 #pragma unroll
-                for (int i = 0; i < kCh; ++i) f[i] *= silu(zc.f32(i));
+                for (int i = 0; i < kCh; ++i) f[i] *= silu<T>(zc.f32(i));
             }
             T *yr = y + t0 * p.channels;
             if constexpr (ODD) {
@@ -437,7 +437,7 @@ __global__ __launch_bounds__(kThreads) void scan_steps_kernel(SelectiveParams p)
         if (p.softplus) s = softplus(s);
         float acc = advance(s, s * uv, bv, cv);
         acc = fmaf(skip, uv, lanes_sum<W>(acc));
-        if (p.z) acc *= silu(zv);
+        if (p.z) acc *= silu<T>(zv);
         if (part == 0) (y + t * p.channels)[d] = from_f32<T>(acc);
         if (p.state_out && t == j) *reinterpret_cast<f32x4 *>(p.state_out + at) = h;
     };
@@ -468,7 +468,7 @@ __global__ __launch_bounds__(kThreads) void scan_steps_kernel(SelectiveParams p)
                                       advance(of_quad<2>(s), of_quad<2>(du), bv[2], cv[2]),
                                       advance(of_quad<3>(s), of_quad<3>(du), bv[3], cv[3])};
                 float r = fmaf(skip, uv, lanes_sum4<W>(acc));
-                if (p.z) r *= silu(zv);
+                if (p.z) r *= silu<T>(zv);
                 if (part < 4) (y + (int64_t)(t + q) * p.channels)[d] = from_f32<T>(r);
             }
         }
