@@ -174,7 +174,9 @@ hipError_t run(const NormParams &p, hipStream_t stream) {
     const int held = p.group_dim < VEC ? 0 : (pieces + gr.lanes - 1) / gr.lanes;
     const int threads = std::max(gr.lanes, 64);
     const int64_t wgs = (parts * gr.lanes + threads - 1) / threads;
-    const unsigned grid = (unsigned)std::min<int64_t>(wgs, (int64_t)1 << 22);
+    // A launch's threads stay below 2^32: 2^31 at most with 1024 per workgroup
+    // (the workgroups take turns where there are more parts).
+    const unsigned grid = (unsigned)std::min<int64_t>(wgs, (int64_t)1 << 21);
     switch (held) {
         case 1: return launch<T, 1>(p, gr, grid, threads, stream);
         case 2: return launch<T, 2>(p, gr, grid, threads, stream);
