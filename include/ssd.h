@@ -357,7 +357,7 @@ typedef enum {
  *                                     init_state); non-NULL exactly when
  *                                     state_out_idx is
  * With a padded batch, j_b = length - 1 gives each sequence's own state.
- * One kernel, no workspace.  Ch <= 2^20. */
+ * One kernel, no workspace.  batch <= 65535, T < 2^31, Ch <= 2^20. */
 ssd_status ssd_causal_conv_fwd(const void *x, const float *weight, const float *bias,
                                const void *init_state, int activation,
                                void *out0, void *out1, void *out2, void *final_state,
@@ -403,7 +403,7 @@ typedef struct {
  *                 contents on entry ignored; may be NULL when that is 0
  * A and every state are 16-byte aligned.  Calls of few sequences and channels
  * share a long sequence out over the GPU (this needs the workspace); the choice
- * depends on the sizes alone. */
+ * depends on the sizes alone.  batch and ngroups <= 65535, T < 2^31, Dm <= 2^20. */
 ssd_status ssd_selective_scan_fwd(const void *u, const void *delta, const float *A,
                                   const void *B, const void *C, const float *D,
                                   const void *z, const float *delta_bias, int delta_softplus,
@@ -481,7 +481,8 @@ typedef struct {
  *   tokens        [b,K+1]    int32  the n accepted drafts, next, then -1; NULL =
  *                                   not returned
  *   workspace     16-byte aligned, ssd_verify_workspace_bytes(...) bytes,
- *                 contents on entry ignored; may be NULL when that is 0 */
+ *                 contents on entry ignored; may be NULL when that is 0
+ * batch <= 65535, K <= 2^20, V < 2^31. */
 ssd_status ssd_verify_drafts(const void *target_probs, const void *draft_probs,
                              const int32_t *draft_tokens, const int32_t *draft_lens,
                              const float *uniforms, int32_t *n_accepted, int32_t *next_token,

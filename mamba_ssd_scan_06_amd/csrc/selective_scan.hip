@@ -16,11 +16,12 @@
 // per (token, channel) instead of per state - softplus, s u, the skip term, the
 // gate, conversions and global accesses - is done once, tile by tile (32
 // tokens), with 8 channels of one token per thread.  The next tile's global
-// loads are in flight during a tile's scan.  Measured: 390-420 us for 8 x 2048
-// tokens of 5120 channels (N 16), 30 VALU instructions per wave and token, 20
-// of them the scan's; the VALU is 90% busy where a compute unit holds three
-// workgroups.  (Reading the next tokens' LDS values ahead into registers was
-// slower: 445-490 us.)
+// loads are in flight during a tile's scan.  Measured: 394 us for 8 x 2048
+// tokens of 5120 channels (N 16; up to 500 in the first sixty calls after an
+// idle time), 31 VALU instructions per wave and token, 20 of them the scan's;
+// the VALU is 92% busy where a compute unit holds three workgroups.  (Reading
+// the next tokens' LDS values ahead into registers was slower: 445-490 us
+// against 400-410.)
 //
 // Few sequences and channels leave most of the GPU idle that way, and the
 // recurrence is serial in tokens.  The tokens are then split into ranges: one
@@ -29,9 +30,9 @@
 // steps; in the second launch each range forms its entering state,
 //     h <- exp(A sum_of_steps) h + range's final state,
 // over the ranges before it (scaled_by_exp2 where A or the steps let that
-// factor grow), and runs in full.  That doubles the work, so
-// ranges are used only where they at least quadruple the workgroups
-// (selective_ranges has the figures).
+// factor grow), and runs in full.  That doubles the work, so ranges are used
+// only where the GPU has room for four times the workgroups (selective_ranges
+// has the figures).
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -532,7 +533,12 @@ void selective_ranges(SelectiveParams &p) {
     // without / with them: 24 workgroups, 200 tokens 27 / 16, 4093 tokens 438 /
     // 61; 80, 100 tokens 15.5 / 13.8, 2048 tokens 223 / 115; 192, 100 tokens
     // 16 / 22; 160, 2048 tokens 228 / 190 with four ranges, 278 with two; 320,
-    // 2048 tokens 304 / 348 with two: hence at least four.)
+    // 2048 tokens 304 / 348 with two: hence room for at least four.)  Whole
+    // tiles may leave three of the four or five asked for, with 129 to 288
+    // tokens on 86 to 181 workgroups; three cost 0.9 to 1.11 of a call without
+    // ranges (us with three / none: N 16, 160 workgroups 192 tokens 28 / 25, 288
+    // tokens 37.5 / 36; 128 workgroups 288 tokens 34 / 35; N 64, 128 workgroups
+    // 160 tokens 55 / 49.5, 288 tokens 77 / 86).
     const int64_t tiles = (p.group_channels + kChannels - 1) / kChannels;
     const int64_t wgs = tiles * p.ngroups * p.batch, held = (p.dstate >= 32 ? 2 : 3) * (int64_t)256;
     const int64_t want = std::min(held / wgs, (p.seqlen + kTile - 1) / kTile);

@@ -319,9 +319,13 @@ void verify_segments(VerifyParams &p) {
     const int64_t want = std::min<int64_t>({kMaxSegments, 1024 / std::max<int64_t>(p.batch, 1), p.vocab / 2048});
     // Two launches pay where a row alone takes three rounds of its workgroup's
     // loads (us with one launch / two: 1 row of 16384 8.0 / 8.2, of 32000 10.1 /
-    // 8.4, of 128256 21.9 / 7.9; 64 rows of 32000 10.6 / 11.1, of 64000 17.4 /
-    // 11.4) and the rows leave compute units idle (128 rows of 128256 32.9 /
-    // 32.2; 256 rows of 50277 15.7 / 22.6).
+    // 8.4, of 128256 21.9 / 7.9; 64 rows of 64000 17.4 / 11.4) and the rows leave
+    // compute units idle (128 rows of 128256 32.9 / 32.2; 256 rows of 50277 15.7 /
+    // 22.6).  The rows at which both are even grow with the row's length: 48 to 64
+    // rows of 32000 (48 10.0 / 9.7, 64 10.0 / 10.2, 96 10.2 / 10.8), about 110 of
+    // 50277 (64 15.3 / 10.7, 96 16.0 / 15.1, 127 17.0 / 17.5), 127 of 128256 (64
+    // 30.7 / 18.8, 96 31.3 / 28.5); 64 for all of them leaves up to a quarter
+    // between 65 and 110 long rows.
     const int64_t rounds = p.vocab / (kThreads * 16);
     p.segments = want >= 2 && rounds >= 3 && p.batch <= 64 ? (int)want : 1;
     p.segment = (p.vocab + p.segments - 1) / p.segments;
