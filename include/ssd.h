@@ -305,8 +305,9 @@ ssd_status ssd_state_correction(void *y, const float *dt, const float *A, const 
 /* ---------------------------------------------------------------------------
  * The operators around the scan in its layer and in its verify loop: the short
  * causal convolution before it, the selective scan with one decay per channel
- * and state index, the gated RMS norm after it, and the verification of
- * drafted tokens that yields the accepted index.  Conventions as above (device
+ * and state index, the gated delta rule, the gated RMS norm after it, the norms
+ * and residual stream between blocks, and the verification of drafted tokens
+ * that yields the accepted index.  Conventions as above (device
  * pointers, stream order, host-side checks before any launch, no allocation),
  * except that inputs named with a stride below need not be dense: strides are
  * in elements, >= 0 (0 repeats a row), and of no account along a dimension of
@@ -327,10 +328,12 @@ typedef struct {
     int64_t x_token_stride;
 } ssd_conv_shape;
 
-/* Activation codes of ssd_causal_conv_fwd. */
+/* Activation codes of ssd_causal_conv_fwd (NONE, SILU) and of
+ * ssd_residual_norm_fwd's gate (all). */
 typedef enum {
     SSD_ACT_NONE = 0,
-    SSD_ACT_SILU = 1   /* v * sigmoid(v) */
+    SSD_ACT_SILU = 1,    /* v * sigmoid(v)                               */
+    SSD_ACT_SIGMOID = 2  /* 1 / (1 + exp(-v)); of a gate only            */
 } ssd_activation;
 
 /* Depthwise causal convolution over tokens, with Ch = the sum of channels:
@@ -492,6 +495,104 @@ ssd_status ssd_verify_drafts(const void *target_probs, const void *draft_probs,
 /* Bytes of workspace ssd_verify_drafts needs; 0 also when the arguments are
  * invalid (ssd_last_error() says why). */
 size_t ssd_verify_workspace_bytes(const ssd_verify_shape *shape, ssd_dtype dtype);
+
+/* Sizes of ssd_gated_delta_fwd.  batch and seqlen may be 0. */
+typedef struct {
+    int64_t batch;     /* b: independent sequences                              */
+    int64_t seqlen;    /* T: tokens per sequence                                */
+    int64_t nheads;    /* H: heads, a multiple of ngroups                       */
+    int64_t headdim;   /* P: values per head, a multiple of 16 up to 256        */
+    int64_t dstate;    /* N: size of a key, a multiple of 16 up to 256          */
+    int64_t ngroups;   /* G: query/key groups; head h reads group h*G/H         */
+    int64_t q_batch_stride, q_token_stride;
+    int64_t k_batch_stride, k_token_stride;
+    int64_t v_batch_stride, v_token_stride;
+    int64_t g_batch_stride, g_token_stride;
+    int64_t beta_batch_stride, beta_token_stride;
+} ssd_delta_shape;
+
+/* The gated delta rule: a matrix state that forgets by exp(g) and replaces what
+ * it holds under a key by beta's share, instead of adding to it as the SSD scan
+ * does.  For every sequence, head h (group gr = h*G/H) and token t:
+ *
+ *     r_t = v[b,t,h,:] - exp(g[b,t,h]) * S_{t-1} k_t           k_t = k[b,t,gr,:]
+ *     S_t = exp(g[b,t,h]) * S_{t-1} + beta[b,t,h] * r_t k_t'
+ *     y[b,t,h,:] = scale * S_t q_t                             q_t = q[b,t,gr,:]
+ *
+ * with S_{-1} = init_state (zeros when absent).  With qk_l2norm, q_t and k_t are
+ * divided by sqrt(sum of their squares + 1e-6) first.
+ *
+ *   q, k          [b,T,G,N]  dtype  strided by batch and token; a token's G*N
+ *                                   values are contiguous
+ *   v             [b,T,H,P]  dtype  strided like them
+ *   g             [b,T,H]    fp32   log decays (<= 0; greater ones are computed
+ *                                   as given), strided by batch and token;
+ *                                   NULL = 0 (no decay)
+ *   beta          [b,T,H]    fp32   strided like g
+ *   init_state    [b,H,P,N]  fp32   NULL = zeros
+ *   y             [b,T,H,P]  dtype  dense, rounded once from fp32
+ *   final_state   [b,H,P,N]  fp32   NULL = not returned; may be init_state itself
+ *   state_out_idx [b]        int32  accepted index j_b in [-1, T-1]; NULL = none
+ *   state_out     [b,H,P,N]  fp32   the state after token j_b (-1: init_state);
+ *                                   non-NULL exactly when state_out_idx is
+ *   workspace     16-byte aligned, ssd_gated_delta_workspace_bytes(...) bytes,
+ *                 contents on entry ignored; may be NULL when that is 0
+ * States are fp32 throughout and 16-byte aligned.  Values are finite; g and beta
+ * need not be bounded, but keys of norm above sqrt(2 / beta) make the rule
+ * itself grow.  A few tokens run token by token, prompts in chunks (this needs
+ * the workspace); the choice depends on the sizes and dtype alone.  With a
+ * padded batch, j_b = length - 1 gives each sequence's own state.
+ * batch, nheads <= 65535, T < 2^31, batch * nheads * ceil(P / 32) < 2^24. */
+ssd_status ssd_gated_delta_fwd(const void *q, const void *k, const void *v, const float *g,
+                               const float *beta, float scale, int qk_l2norm,
+                               const float *init_state, void *y, float *final_state,
+                               const int32_t *state_out_idx, float *state_out,
+                               const ssd_delta_shape *shape, ssd_dtype dtype,
+                               void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace ssd_gated_delta_fwd needs; 0 also when the arguments are
+ * invalid (ssd_last_error() says why). */
+size_t ssd_gated_delta_workspace_bytes(const ssd_delta_shape *shape, ssd_dtype dtype);
+
+/* Sizes of ssd_residual_norm_fwd.  batch and seqlen may be 0. */
+typedef struct {
+    int64_t batch, seqlen;  /* b, T: one row per token                           */
+    int64_t dim;            /* elements per row                                  */
+    int64_t x_batch_stride, x_token_stride;
+    int64_t residual_batch_stride, residual_token_stride;
+    int64_t gate_batch_stride, gate_token_stride;  /* token stride 0: one gate per sequence */
+} ssd_residual_norm_shape;
+
+/* What stands between two blocks: the norm after a block, its gate and scale,
+ * the residual stream, and the norm before the next block:
+ *
+ *     n   = post_norm ? x / rms(x) * post_weight : x
+ *     h   = residual_scale * residual + branch_scale * layer_scale * act(gate) * n
+ *     out = h / rms(h) * weight
+ *
+ * with rms(v) = sqrt(mean(v^2) + eps) over the row; everything in fp32, h
+ * rounded once where it is stored (out comes from h before that rounding).
+ * What is absent is left out.
+ *
+ *   x            [b,T,dim]  dtype         the block's output, strided
+ *   residual     [b,T,dim]  stream_dtype  strided; NULL = none (h is the branch)
+ *   gate         [b,T,dim]  dtype         strided; NULL = none
+ *   gate_activation         SSD_ACT_*     of the gate
+ *   post_weight  [dim]      fp32          NULL = ones; only with post_norm
+ *   layer_scale  [dim]      fp32          NULL = ones
+ *   weight       [dim]      fp32          NULL = ones
+ *   out          [b,T,dim]  dtype         dense; may be x itself where that is dense
+ *   residual_out [b,T,dim]  stream_dtype  h, dense; NULL = not returned; may be
+ *                                         residual itself where that is dense
+ *   eps                     >= 0 and finite (with 0 a row of zeros gives NaN)
+ * stream_dtype is dtype or fp32.  One kernel, no workspace.  dim <= 2^20,
+ * b*T < 2^31. */
+ssd_status ssd_residual_norm_fwd(const void *x, const void *residual, const void *gate,
+                                 int gate_activation, int post_norm, const float *post_weight,
+                                 const float *layer_scale, float residual_scale,
+                                 float branch_scale, const float *weight, float eps, void *out,
+                                 void *residual_out, const ssd_residual_norm_shape *shape,
+                                 ssd_dtype dtype, ssd_dtype stream_dtype, void *hip_stream);
 
 /* Static description of a status code. */
 const char *ssd_status_string(ssd_status status);

@@ -19,6 +19,7 @@ __all__ = [
     "ssd_get_workspace_layout", "ssd_select_path", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_ex",
     "ssd_chunk_scan_fwd_noalloc", "ssd_state_correction", "ssd_causal_conv_fwd", "ssd_selective_scan_fwd",
     "ssd_selective_scan_workspace_bytes", "ssd_gated_norm_fwd", "ssd_verify_drafts", "ssd_verify_workspace_bytes",
+    "ssd_gated_delta_fwd", "ssd_gated_delta_workspace_bytes", "ssd_residual_norm_fwd",
     "SSD_NOALLOC_SCRATCH_BYTES", "workspace_views", "library_path", "SSD_PATH_AUTO", "SSD_PATH_ONE_CHUNK", "SSD_PATH_SINGLE_PASS",
     "SSD_PATH_CHUNK_PARALLEL",
 ]
@@ -81,6 +82,19 @@ class ssd_verify_shape(ctypes.Structure):
                                               "target_row_stride", "draft_batch_stride", "draft_row_stride")]
 
 
+class ssd_delta_shape(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in (
+        "batch", "seqlen", "nheads", "headdim", "dstate", "ngroups", "q_batch_stride", "q_token_stride",
+        "k_batch_stride", "k_token_stride", "v_batch_stride", "v_token_stride", "g_batch_stride", "g_token_stride",
+        "beta_batch_stride", "beta_token_stride")]
+
+
+class ssd_residual_norm_shape(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int64) for k in (
+        "batch", "seqlen", "dim", "x_batch_stride", "x_token_stride", "residual_batch_stride",
+        "residual_token_stride", "gate_batch_stride", "gate_token_stride")]
+
+
 class SsdError(RuntimeError):
     def __init__(self, status: int, detail: str):
         self.status = status
@@ -137,6 +151,15 @@ def _load():
     lib.ssd_verify_drafts.restype = i32
     lib.ssd_verify_workspace_bytes.argtypes = [ver, i32]
     lib.ssd_verify_workspace_bytes.restype = sz
+    dlt = ctypes.POINTER(ssd_delta_shape)
+    f32 = ctypes.c_float
+    lib.ssd_gated_delta_fwd.argtypes = [vp, vp, vp, vp, vp, f32, i32, vp, vp, vp, vp, vp, dlt, i32, vp, sz, vp]
+    lib.ssd_gated_delta_fwd.restype = i32
+    lib.ssd_gated_delta_workspace_bytes.argtypes = [dlt, i32]
+    lib.ssd_gated_delta_workspace_bytes.restype = sz
+    lib.ssd_residual_norm_fwd.argtypes = [vp, vp, vp, i32, i32, vp, vp, f32, f32, vp, f32, vp, vp,
+                                          ctypes.POINTER(ssd_residual_norm_shape), i32, i32, vp]
+    lib.ssd_residual_norm_fwd.restype = i32
     lib.ssd_status_string.argtypes = [i32]
     lib.ssd_status_string.restype = ctypes.c_char_p
     lib.ssd_last_error.argtypes = []
@@ -152,6 +175,8 @@ def _load():
         fast.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.ssd_causal_conv_fwd, lib.ssd_selective_scan_fwd, lib.ssd_selective_scan_workspace_bytes,
             lib.ssd_gated_norm_fwd, lib.ssd_verify_drafts, lib.ssd_verify_workspace_bytes)))
+        fast.bind_blocks(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.ssd_gated_delta_fwd, lib.ssd_gated_delta_workspace_bytes, lib.ssd_residual_norm_fwd)))
         fast.raw_stream = torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None
         _fast = fast
     _lib = lib
@@ -742,6 +767,173 @@ def ssd_verify_drafts(target_probs, draft_tokens, uniforms, draft_probs=None, dr
                                  _addr(uniforms), _addr(n_accepted), _addr(next_token), _addr(tokens), ref, code,
                                  _addr(workspace), ws_bytes, _raw_stream(torch, dev)))
     return n_accepted, next_token, tokens
+
+
+def ssd_gated_delta_workspace_bytes(shape: ssd_delta_shape, dtype: int) -> int:
+    return int(_load().ssd_gated_delta_workspace_bytes(ctypes.byref(shape), int(dtype)))
+
+
+def ssd_gated_delta_fwd(q, k, v, g, beta, init_state=None, state_out_idx=None, *, scale=None, qk_l2norm: bool = False,
+                        y=None, final_state=None, return_final_state: bool = True, state_out=None, workspace=None,
+                        stream=None):
+    """Gated delta rule (see ssd_gated_delta_fwd in include/ssd.h).
+
+    q, k [b,T,G,N] and v [b,T,H,P] bf16|fp32 (strides free by batch and token,
+    e.g. the convolution's outputs), g [b,T,H] fp32 log decays or None for
+    none, beta [b,T,H] fp32 (strides free as well), init_state [b,H,P,N] fp32
+    or None, state_out_idx [b] int32 or None; scale of the outputs, N ** -0.5
+    when None; with qk_l2norm each q and k is normalised first.  Outputs and
+    the workspace are allocated when not given; final_state may be init_state
+    itself.  Returns (y, final_state or None, state_out or None).  Errors as
+    for ssd_chunk_scan_fwd.
+    """
+    if _fast is not None and q.is_cuda and stream is None and y is None and state_out is None and workspace is None:
+        r = _fast.delta(q, k, v, g, beta, init_state, state_out_idx, scale, qk_l2norm, final_state,
+                        return_final_state, _fast.raw_stream(q.device.index))
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(r)
+    import torch
+
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k must be [b,T,G,N] and v [b,T,H,P]")
+    if _elsewhere(torch, q, stream):
+        with _scope(torch, q, stream):
+            return ssd_gated_delta_fwd(q, k, v, g, beta, init_state, state_out_idx, scale=scale, qk_l2norm=qk_l2norm,
+                                       y=y, final_state=final_state, return_final_state=return_final_state,
+                                       state_out=state_out, workspace=workspace)
+    f32 = torch.float32
+    b, T, G, N = q.shape
+    H, P = v.shape[2], v.shape[3]
+    code, dtype, dev = _dtype_code(torch, q, "q"), q.dtype, q.device
+    sq = _strided("q", q, q.shape, dtype, dev, 2)
+    sk = _strided("k", k, q.shape, dtype, dev, 2)
+    sv = _strided("v", v, (b, T, H, P), dtype, dev, 2)
+    sg = _strided("g", g, (b, T, H), f32, dev) if g is not None else (0, 0)
+    sb = _strided("beta", beta, (b, T, H), f32, dev)
+    state = (b, H, P, N)
+    if init_state is not None:
+        _dense("init_state", init_state, state, f32, dev)
+    if state_out_idx is not None:
+        _dense("state_out_idx", state_out_idx, (b,), torch.int32, dev)
+    elif state_out is not None:
+        raise ValueError("state_out needs state_out_idx")
+    if y is not None:
+        _dense("y", y, (b, T, H, P), dtype, dev)
+    if final_state is not None:
+        _dense("final_state", final_state, state, f32, dev)
+    if state_out is not None:
+        _dense("state_out", state_out, state, f32, dev)
+    if workspace is not None:
+        _dense("workspace", workspace, (workspace.numel(),), torch.uint8, dev)
+    if not q.is_cuda:
+        raise ValueError(f"tensors must be on a GPU device, q is on {dev}")
+    if scale is None:
+        scale = N ** -0.5 if N > 0 else 1.0
+    lib = _load()
+    shape = ssd_delta_shape(b, T, H, P, N, G, sq[0], sq[1], sk[0], sk[1], sv[0], sv[1], sg[0], sg[1], sb[0], sb[1])
+    ref = ctypes.byref(shape)
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+    else:
+        ws_bytes = lib.ssd_gated_delta_workspace_bytes(ref, code)
+        if ws_bytes > 0:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    if y is None:
+        y = v.new_empty((b, T, H, P))
+    if final_state is None and return_final_state:
+        final_state = beta.new_empty(state)
+    if state_out is None and state_out_idx is not None:
+        state_out = beta.new_empty(state)
+    _check(lib.ssd_gated_delta_fwd(_addr(q), _addr(k), _addr(v), _addr(g), _addr(beta), scale, 1 if qk_l2norm else 0,
+                                   _addr(init_state), _addr(y), _addr(final_state), _addr(state_out_idx),
+                                   _addr(state_out), ref, code, _addr(workspace), ws_bytes, _raw_stream(torch, dev)))
+    return y, final_state, state_out
+
+
+ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
+
+
+def ssd_residual_norm_fwd(x, residual=None, weight=None, *, post_norm: bool = False, post_weight=None, gate=None,
+                          gate_activation=None, layer_scale=None, residual_scale: float = 1.0,
+                          branch_scale: float = 1.0, eps: float = 1e-5, out=None, residual_out=None,
+                          return_residual: bool = True, stream=None):
+    """Norms before and after a block with its gate, scales and the residual
+    stream (see ssd_residual_norm_fwd in include/ssd.h).
+
+    x [dim], [T,dim], [b,T,dim] or more leading dimensions (those before the
+    last two merge into one) bf16|fp32, the block's output; residual like it,
+    of x's type or fp32, or None; gate like x, or with one token for all of a
+    sequence's, or None; gate_activation None, "silu" or "sigmoid"; weight,
+    post_weight (with post_norm) and layer_scale [dim] fp32 or None.  Batch and
+    token strides of x, residual and gate are free.  out (dense, may be x
+    itself where that is dense) and residual_out (residual's type, x's without
+    one; may be residual itself) are allocated when not given.  Returns (out,
+    residual_out or None).  Errors as for ssd_chunk_scan_fwd.
+    """
+    if _fast is not None and x.is_cuda and stream is None and out is None and residual_out is None and return_residual:
+        r = _fast.residual_norm(x, residual, weight, post_norm, post_weight, gate, gate_activation, layer_scale,
+                                residual_scale, branch_scale, eps, _fast.raw_stream(x.device.index))
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            _check(r)
+    import torch
+
+    if x.dim() < 1:
+        raise ValueError("x must be [..., dim]")
+    if _elsewhere(torch, x, stream):
+        with _scope(torch, x, stream):
+            return ssd_residual_norm_fwd(x, residual, weight, post_norm=post_norm, post_weight=post_weight, gate=gate,
+                                         gate_activation=gate_activation, layer_scale=layer_scale,
+                                         residual_scale=residual_scale, branch_scale=branch_scale, eps=eps, out=out,
+                                         residual_out=residual_out, return_residual=return_residual)
+    f32 = torch.float32
+    code, dtype, dev = _dtype_code(torch, x), x.dtype, x.device
+    dim = x.shape[-1]
+    stream_type = dtype if residual is None else residual.dtype
+    if stream_type is not dtype and stream_type is not f32:
+        raise TypeError(f"residual must be {dtype} or {f32}, got {stream_type}")
+    if residual is None and residual_out is not None and residual_out.dtype is f32:
+        stream_type = f32
+    if gate_activation not in ACTIVATIONS:
+        raise ValueError(f"gate_activation must be None, 'silu' or 'sigmoid', got {gate_activation!r}")
+    if post_weight is not None and not post_norm:
+        raise ValueError("post_weight needs post_norm")
+    _strided("x", x, x.shape, dtype, dev)
+    if residual is not None:
+        _strided("residual", residual, x.shape, stream_type, dev)
+    if gate is not None:
+        if x.dim() > 1 and gate.shape == (*x.shape[:-2], 1, dim):
+            gate = gate.expand(x.shape)
+        _strided("gate", gate, x.shape, dtype, dev)
+    for name, t in (("weight", weight), ("post_weight", post_weight), ("layer_scale", layer_scale)):
+        if t is not None:
+            _dense(name, t, (dim,), f32, dev)
+    if out is not None:
+        _dense("out", out, x.shape, dtype, dev)
+    if residual_out is not None:
+        _dense("residual_out", residual_out, x.shape, stream_type, dev)
+    if not x.is_cuda:
+        raise ValueError(f"tensors must be on a GPU device, x is on {dev}")
+    lib = _load()
+    if out is None:
+        out = x.new_empty(x.shape)
+    if residual_out is None and return_residual:
+        residual_out = x.new_empty(x.shape, dtype=stream_type)
+    T = x.shape[-2] if x.dim() > 1 else 1
+    b = x.numel() // (T * dim) if T * dim else 0
+    sx = _two_levels("x", x, b, T)
+    sr = _two_levels("residual", residual, b, T) if residual is not None else (0, 0)
+    sg = _two_levels("gate", gate, b, T) if gate is not None else (0, 0)
+    shape = ssd_residual_norm_shape(b, T, dim, sx[0], sx[1], sr[0], sr[1], sg[0], sg[1])
+    _check(lib.ssd_residual_norm_fwd(_addr(x), _addr(residual), _addr(gate), ACTIVATIONS[gate_activation],
+                                     1 if post_norm else 0, _addr(post_weight), _addr(layer_scale), residual_scale,
+                                     branch_scale, _addr(weight), eps, _addr(out), _addr(residual_out),
+                                     ctypes.byref(shape), code, SSD_DTYPE_F32 if stream_type is f32 else code,
+                                     _raw_stream(torch, dev)))
+    return out, residual_out
 
 
 def workspace_views(workspace, shape: ssd_shape, chunk_size: int, dtype: int):

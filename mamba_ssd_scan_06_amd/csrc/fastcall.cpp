@@ -16,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <initializer_list>
 
 #include "ssd.h"
@@ -28,6 +29,9 @@ decltype(&ssd_selective_scan_workspace_bytes) g_scan_bytes;
 decltype(&ssd_gated_norm_fwd) g_norm;
 decltype(&ssd_verify_drafts) g_verify;
 decltype(&ssd_verify_workspace_bytes) g_verify_bytes;
+decltype(&ssd_gated_delta_fwd) g_delta;
+decltype(&ssd_gated_delta_workspace_bytes) g_delta_bytes;
+decltype(&ssd_residual_norm_fwd) g_residual_norm;
 
 // An argument that is a tensor or None (anything else does not fit).
 struct Arg {
@@ -281,7 +285,127 @@ PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// Addresses of the C entry points, in the order of the pointers above.
+// A float option given as a Python float (ints and others take the long way).
+bool real(PyObject *o, float *v) {
+    if (!PyFloat_CheckExact(o)) return false;
+    *v = (float)PyFloat_AS_DOUBLE(o);
+    return true;
+}
+
+// q, k, v, g, beta, init_state, state_out_idx, scale, qk_l2norm, final_state, return_final_state, stream
+PyObject *delta(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        if (n != 12 || !PyBool_Check(a[8]) || !PyBool_Check(a[10])) return none();
+        const Arg q(a[0]), k(a[1]), v(a[2]), g(a[3]), beta(a[4]), init(a[5]), idx(a[6]);
+        Arg fin(a[9]);
+        const int code = code_of(q);
+        if (code < 0 || q.t.dim() != 4 || !v.ok || !v.t.defined() || v.t.dim() != 4 || !beta.ok || !beta.t.defined())
+            return none();
+        const int64_t b = q.t.size(0), T = q.t.size(1), G = q.t.size(2), N = q.t.size(3), H = v.t.size(2),
+                      P = v.t.size(3);
+        const auto type = q.t.scalar_type();
+        const auto dev = q.t.device();
+        if (b == 0 || T == 0 || G == 0 || N == 0 || H == 0 || P == 0 || !strided(q, {b, T, G, N}, type, dev, true, 2) ||
+            !strided(k, {b, T, G, N}, type, dev, true, 2) || !strided(v, {b, T, H, P}, type, dev, true, 2) ||
+            !strided(g, {b, T, H}, at::kFloat, dev, false) || !strided(beta, {b, T, H}, at::kFloat, dev, true) ||
+            !dense(init, {b, H, P, N}, at::kFloat, dev) || !dense(idx, {b}, at::kInt, dev) ||
+            !dense(fin, {b, H, P, N}, at::kFloat, dev))
+            return none();
+        float scale;
+        if (a[7] == Py_None) scale = (float)(1.0 / std::sqrt((double)N));
+        else if (!real(a[7], &scale)) return none();
+        const bool l2 = a[8] == Py_True, want_final = a[10] == Py_True;
+        void *const stream = stream_of(a[11]);
+        at::Tensor y, at_j, ws;
+        ssd_status r;
+        {
+            const Unlocked unlocked;
+            auto st = [](const Arg &t, int d) { return t.t.defined() ? t.t.stride(d) : 0; };
+            ssd_delta_shape s = {b,        T,        H,        P,        N,        G,        st(q, 0),    st(q, 1),
+                                 st(k, 0), st(k, 1), st(v, 0), st(v, 1), st(g, 0), st(g, 1), st(beta, 0), st(beta, 1)};
+            const size_t bytes = g_delta_bytes(&s, (ssd_dtype)code);
+            y = at::empty({b, T, H, P}, v.t.options());
+            if (!fin.t.defined() && want_final) fin.t = at::empty({b, H, P, N}, beta.t.options());
+            if (idx.t.defined()) at_j = at::empty({b, H, P, N}, beta.t.options());
+            if (bytes > 0) ws = at::empty({(int64_t)bytes}, beta.t.options().dtype(at::kByte));
+            auto p = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
+            r = g_delta(q.ptr(), k.ptr(), v.ptr(), (const float *)g.ptr(), (const float *)beta.ptr(), scale, l2,
+                        (const float *)init.ptr(), y.data_ptr(), (float *)fin.ptr(), (const int32_t *)idx.ptr(),
+                        (float *)p(at_j), &s, (ssd_dtype)code, p(ws), bytes, stream);
+        }
+        if (r != SSD_OK) return PyLong_FromLong(r);
+        return three(wrap(y), wrap(fin.t), wrap(at_j));
+    });
+}
+
+// x, residual, weight, post_norm, post_weight, gate, gate_activation, layer_scale, residual_scale, branch_scale, eps,
+// stream; x of two or three dimensions
+PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        float r_scale, b_scale, eps;
+        if (n != 12 || !PyBool_Check(a[3]) || !real(a[8], &r_scale) || !real(a[9], &b_scale) || !real(a[10], &eps))
+            return none();
+        const Arg x(a[0]), res(a[1]), w(a[2]), post(a[4]), gate(a[5]), layer(a[7]);
+        const int code = code_of(x);
+        if (code < 0 || (x.t.dim() != 2 && x.t.dim() != 3) || x.t.numel() == 0 || !res.ok || !gate.ok) return none();
+        const bool two = x.t.dim() == 2;
+        const int64_t b = two ? 1 : x.t.size(0), T = x.t.size(-2), dim = x.t.size(-1);
+        const auto dev = x.t.device();
+        if (x.t.stride(-1) != 1 || !dense(w, {dim}, at::kFloat, dev) || !dense(post, {dim}, at::kFloat, dev) ||
+            !dense(layer, {dim}, at::kFloat, dev))
+            return none();
+        auto like = [&](const at::Tensor &t) { return t.sizes() == x.t.sizes() && t.device() == dev && t.stride(-1) == 1; };
+        auto type = x.t.scalar_type();
+        if (gate.t.defined() && (!like(gate.t) || gate.t.scalar_type() != type)) return none();
+        if (res.t.defined()) {
+            if (!like(res.t) || (res.t.scalar_type() != type && res.t.scalar_type() != at::kFloat)) return none();
+            type = res.t.scalar_type();
+        }
+        int act = SSD_ACT_NONE;
+        if (a[6] != Py_None) {
+            if (!PyUnicode_CheckExact(a[6])) return none();
+            if (PyUnicode_CompareWithASCIIString(a[6], "silu") == 0) act = SSD_ACT_SILU;
+            else if (PyUnicode_CompareWithASCIIString(a[6], "sigmoid") == 0) act = SSD_ACT_SIGMOID;
+            else return none();
+        }
+        const bool post_norm = a[3] == Py_True;
+        if (post.t.defined() && !post_norm) return none();
+        void *const stream = stream_of(a[11]);
+        at::Tensor out, h;
+        ssd_status st;
+        {
+            const Unlocked unlocked;
+            out = at::empty(x.t.sizes(), x.t.options());
+            h = at::empty(x.t.sizes(), x.t.options().dtype(type));
+            auto bs = [&](const Arg &t) { return !t.t.defined() || two ? 0 : t.t.stride(0); };
+            auto ts = [&](const Arg &t) { return t.t.defined() ? t.t.stride(-2) : 0; };
+            ssd_residual_norm_shape s = {b, T, dim, bs(x), ts(x), bs(res), ts(res), bs(gate), ts(gate)};
+            st = g_residual_norm(x.ptr(), res.ptr(), gate.ptr(), act, post_norm, (const float *)post.ptr(),
+                                 (const float *)layer.ptr(), r_scale, b_scale, (const float *)w.ptr(), eps,
+                                 out.data_ptr(), h.data_ptr(), &s, (ssd_dtype)code,
+                                 type == at::kFloat ? SSD_DTYPE_F32 : SSD_DTYPE_BF16, stream);
+        }
+        if (st != SSD_OK) return PyLong_FromLong(st);
+        PyObject *p = wrap(out), *q = wrap(h), *r = p && q ? PyTuple_Pack(2, p, q) : nullptr;
+        Py_XDECREF(p);
+        Py_XDECREF(q);
+        return r;
+    });
+}
+
+PyObject *bind_blocks(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    if (n != 3) {
+        PyErr_SetString(PyExc_TypeError, "bind_blocks takes three addresses");
+        return nullptr;
+    }
+    g_delta = (decltype(g_delta))PyLong_AsVoidPtr(a[0]);
+    g_delta_bytes = (decltype(g_delta_bytes))PyLong_AsVoidPtr(a[1]);
+    g_residual_norm = (decltype(g_residual_norm))PyLong_AsVoidPtr(a[2]);
+    if (PyErr_Occurred()) return nullptr;
+    Py_RETURN_NONE;
+}
+
+// Addresses of the other C entry points, in the order of the pointers above.
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 6) {
         PyErr_SetString(PyExc_TypeError, "bind takes six addresses");
@@ -299,6 +423,9 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 #define FAST(f) (PyCFunction)(void (*)())f, METH_FASTCALL
 PyMethodDef g_methods[] = {{"bind", FAST(bind), "addresses of the C entry points"},
+                           {"bind_blocks", FAST(bind_blocks), "addresses of the gated delta rule and the residual norm"},
+                           {"delta", FAST(delta), "ssd_gated_delta_fwd"},
+                           {"residual_norm", FAST(residual_norm), "ssd_residual_norm_fwd"},
                            {"conv", FAST(conv), "ssd_causal_conv_fwd"},
                            {"scan", FAST(scan), "ssd_selective_scan_fwd"},
                            {"norm", FAST(norm), "ssd_gated_norm_fwd"},

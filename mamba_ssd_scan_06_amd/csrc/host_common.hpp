@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "kernels.hpp"
 #include "ssd.h"
 
 namespace ssd {
@@ -53,4 +54,65 @@ inline int64_t product(int64_t a, int64_t b, int64_t c = 1, int64_t d = 1) {
     return r;
 }
 
+// Argument checks of the operators around the scan.
+namespace host {
+
+constexpr int64_t kMaxBatch = 65535;             // a grid dimension
+constexpr int64_t kMaxTokens = (int64_t)1 << 31;  // token indices fit 32 bits
+constexpr int64_t kMaxWide = (int64_t)1 << 20;    // channels, norm dims
+
+inline size_t elem_size(ssd_dtype dtype) { return dtype == SSD_DTYPE_BF16 ? 2 : 4; }
+inline Elem elem(ssd_dtype dtype) { return dtype == SSD_DTYPE_BF16 ? Elem::BF16 : Elem::F32; }
+
+inline ssd_status check_dtype(ssd_dtype dtype) {
+    if (dtype != SSD_DTYPE_F32 && dtype != SSD_DTYPE_BF16) return fail(SSD_ERR_ARGS, "unknown dtype %d", (int)dtype);
+    return SSD_OK;
+}
+
+struct Ptr {
+    const char *name;
+    const void *p;
+    size_t align;
+};
+
+template <int K>
+ssd_status check_align(const Ptr (&ptrs)[K]) {
+    for (const Ptr &q : ptrs)
+        if ((uintptr_t)q.p % q.align != 0) return fail(SSD_ERR_ALIGN, "%s is not %zu-byte aligned", q.name, q.align);
+    return SSD_OK;
+}
+
+// An output that may be one of the inputs itself (an in-place update).
+struct InPlace {
+    int out, in;
+};
+
+// No output may overlap an input or another output, except the allowed pairs
+// of identical pointers.
+template <int NO, int NI, int NA>
+ssd_status check_alias(const Range (&outs)[NO], const Range (&ins)[NI], const InPlace (&allowed)[NA]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int k = 0; k < NI; ++k) {
+            bool same = false;
+            for (const InPlace &a : allowed)
+                same = same || (a.out == i && a.in == k && outs[i].lo == ins[k].lo && outs[i].hi == ins[k].hi);
+            if (!same && overlaps(outs[i], ins[k]))
+                return fail(SSD_ERR_ALIAS, "%s overlaps %s", outs[i].name, ins[k].name);
+        }
+        for (int k = i + 1; k < NO; ++k)
+            if (overlaps(outs[i], outs[k])) return fail(SSD_ERR_ALIAS, "%s overlaps %s", outs[i].name, outs[k].name);
+    }
+    return SSD_OK;
+}
+
+// A stride of a dimension without a second index is never used: 0 keeps it
+// out of the offsets.
+inline int64_t used_stride(int64_t n, int64_t stride) { return n > 1 ? stride : 0; }
+
+inline ssd_status launched(const char *what, hipError_t r) {
+    if (r != hipSuccess) return fail(SSD_ERR_HIP, "%s launch failed: %s", what, hipGetErrorString(r));
+    return SSD_OK;
+}
+
+}  // namespace host
 }  // namespace ssd

@@ -135,6 +135,37 @@ struct NormParams {
 };
 hipError_t launch_gated_norm(const NormParams &p, Elem e, hipStream_t stream);
 
+// Gated delta rule (ssd_gated_delta_fwd).
+struct DeltaParams {
+    const void *q, *k, *v;      // strided
+    const float *g, *beta;      // strided; g may be null
+    const float *init_state;    // [b,H,P,N] or null
+    void *y;                    // [b,T,H,P]
+    float *final_state;         // [b,H,P,N] or null
+    const int32_t *state_out_idx;
+    float *state_out;           // [b,H,P,N] or null
+    int64_t batch, seqlen;
+    int64_t q_bs, q_ts, k_bs, k_ts, v_bs, v_ts, g_bs, g_ts, beta_bs, beta_ts;
+    int nheads, headdim, dstate, ngroups, heads_per_group;
+    float scale;
+    int l2norm;
+};
+hipError_t launch_delta_tokens(const DeltaParams &p, Elem e, hipStream_t stream);
+
+// Norms before and after a block (ssd_residual_norm_fwd).
+struct ResidualNormParams {
+    const void *x, *residual, *gate;  // strided; residual and gate may be null
+    const float *post_weight, *layer_scale, *weight;  // [dim] or null
+    void *out;                        // [b,T,dim]
+    void *residual_out;               // [b,T,dim] or null
+    int64_t rows, seqlen;             // rows = b * T
+    int64_t x_bs, x_ts, r_bs, r_ts, gate_bs, gate_ts;
+    int dim;
+    int activation, post_norm;
+    float residual_scale, branch_scale, eps;
+};
+hipError_t launch_residual_norm(const ResidualNormParams &p, Elem e, Elem stream_elem, hipStream_t stream);
+
 // Verification of drafted tokens (ssd_verify_drafts).
 struct VerifyParams {
     const void *target, *draft;  // strided; draft may be null

@@ -9,69 +9,12 @@
 
 namespace {
 
+using namespace ssd::host;
 using ssd::extent3;
 using ssd::fail;
-using ssd::overlaps;
 using ssd::product;
 using ssd::Range;
 using ssd::range;
-
-constexpr int64_t kMaxBatch = 65535;             // a grid dimension
-constexpr int64_t kMaxTokens = (int64_t)1 << 31;  // token indices fit 32 bits
-constexpr int64_t kMaxWide = (int64_t)1 << 20;    // channels, norm dims
-
-size_t elem_size(ssd_dtype dtype) { return dtype == SSD_DTYPE_BF16 ? 2 : 4; }
-ssd::Elem elem(ssd_dtype dtype) { return dtype == SSD_DTYPE_BF16 ? ssd::Elem::BF16 : ssd::Elem::F32; }
-
-ssd_status check_dtype(ssd_dtype dtype) {
-    if (dtype != SSD_DTYPE_F32 && dtype != SSD_DTYPE_BF16) return fail(SSD_ERR_ARGS, "unknown dtype %d", (int)dtype);
-    return SSD_OK;
-}
-
-struct Ptr {
-    const char *name;
-    const void *p;
-    size_t align;
-};
-
-template <int K>
-ssd_status check_align(const Ptr (&ptrs)[K]) {
-    for (const Ptr &q : ptrs)
-        if ((uintptr_t)q.p % q.align != 0) return fail(SSD_ERR_ALIGN, "%s is not %zu-byte aligned", q.name, q.align);
-    return SSD_OK;
-}
-
-// An output that may be one of the inputs itself (an in-place update).
-struct InPlace {
-    int out, in;
-};
-
-// No output may overlap an input or another output, except the allowed pairs
-// of identical pointers.
-template <int NO, int NI, int NA>
-ssd_status check_alias(const Range (&outs)[NO], const Range (&ins)[NI], const InPlace (&allowed)[NA]) {
-    for (int i = 0; i < NO; ++i) {
-        for (int k = 0; k < NI; ++k) {
-            bool same = false;
-            for (const InPlace &a : allowed)
-                same = same || (a.out == i && a.in == k && outs[i].lo == ins[k].lo && outs[i].hi == ins[k].hi);
-            if (!same && overlaps(outs[i], ins[k]))
-                return fail(SSD_ERR_ALIAS, "%s overlaps %s", outs[i].name, ins[k].name);
-        }
-        for (int k = i + 1; k < NO; ++k)
-            if (overlaps(outs[i], outs[k])) return fail(SSD_ERR_ALIAS, "%s overlaps %s", outs[i].name, outs[k].name);
-    }
-    return SSD_OK;
-}
-
-// A stride of a dimension without a second index is never used: 0 keeps it
-// out of the offsets.
-int64_t used_stride(int64_t n, int64_t stride) { return n > 1 ? stride : 0; }
-
-ssd_status launched(const char *what, hipError_t r) {
-    if (r != hipSuccess) return fail(SSD_ERR_HIP, "%s launch failed: %s", what, hipGetErrorString(r));
-    return SSD_OK;
-}
 
 ssd_status check_selective(const ssd_selective_shape *s, ssd_dtype dtype) {
     if (!s) return fail(SSD_ERR_NULL, "shape is NULL");
