@@ -542,7 +542,8 @@ typedef struct {
  * itself grow.  A few tokens run token by token, prompts in chunks (this needs
  * the workspace); the choice depends on the sizes and dtype alone.  With a
  * padded batch, j_b = length - 1 gives each sequence's own state.
- * batch, nheads <= 65535, T < 2^31, batch * nheads * ceil(P / 32) < 2^24. */
+ * batch, nheads <= 65535, T < 2^31, batch * nheads * ceil(P / 32) < 2^24,
+ * batch * nheads * ceil(T / 32) < 2^26. */
 ssd_status ssd_gated_delta_fwd(const void *q, const void *k, const void *v, const float *g,
                                const float *beta, float scale, int qk_l2norm,
                                const float *init_state, void *y, float *final_state,

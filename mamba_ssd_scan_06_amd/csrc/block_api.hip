@@ -16,6 +16,9 @@ using ssd::product;
 using ssd::Range;
 using ssd::range;
 
+// Calls of more tokens run in chunks.
+constexpr int64_t kDeltaTokens = 16;
+
 ssd_status check_delta(const ssd_delta_shape *s, ssd_dtype dtype) {
     if (!s) return fail(SSD_ERR_NULL, "shape is NULL");
     ssd_status st = check_dtype(dtype);
@@ -33,6 +36,9 @@ ssd_status check_delta(const ssd_delta_shape *s, ssd_dtype dtype) {
         s->batch * s->nheads * ((s->headdim + 31) / 32) >= ((int64_t)1 << 24))
         return fail(SSD_ERR_UNSUPPORTED, "problem too large (batch and nheads <= 65535, seqlen < 2^31, "
                                          "batch * nheads * ceil(headdim / 32) < 2^24)");
+    // The chunks' waves are one launch of fewer than 2^32 threads.
+    if (s->batch * s->nheads * ((s->seqlen + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk) >= ((int64_t)1 << 26))
+        return fail(SSD_ERR_UNSUPPORTED, "problem too large (batch * nheads * ceil(seqlen / 32) < 2^26)");
     return SSD_OK;
 }
 
@@ -55,7 +61,18 @@ ssd::DeltaParams delta_params(const ssd_delta_shape *s) {
     p.g_ts = used_stride(s->seqlen, s->g_token_stride);
     p.beta_bs = used_stride(s->batch, s->beta_batch_stride);
     p.beta_ts = used_stride(s->seqlen, s->beta_token_stride);
+    p.nchunks = s->seqlen > kDeltaTokens ? (s->seqlen + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk : 0;
     return p;
+}
+
+// Byte offset of the accepted index's tables behind the chunks', and all.
+struct DeltaWorkspace {
+    size_t at_off, total;
+};
+DeltaWorkspace delta_workspace(const ssd::DeltaParams &p, ssd_dtype dtype) {
+    if (p.nchunks == 0) return {0, 0};
+    const size_t bh = (size_t)p.batch * p.nheads, packs = bh * p.nchunks * ssd::delta_pack_bytes(elem(dtype));
+    return {packs, packs + bh * ssd::delta_at_bytes()};
 }
 
 }  // namespace
@@ -64,7 +81,7 @@ extern "C" {
 
 size_t ssd_gated_delta_workspace_bytes(const ssd_delta_shape *shape, ssd_dtype dtype) {
     if (check_delta(shape, dtype) != SSD_OK) return 0;
-    return 0;
+    return delta_workspace(delta_params(shape), dtype).total;
 }
 
 ssd_status ssd_gated_delta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
@@ -88,7 +105,8 @@ ssd_status ssd_gated_delta_fwd(const void *q, const void *k, const void *v, cons
     if (b > 0 && T > 0 && (!q || !k || !v || !beta || !y))
         return fail(SSD_ERR_NULL, "q, k, v, beta and y are required");
     ssd::DeltaParams p = delta_params(s);
-    const size_t ws_need = ssd_gated_delta_workspace_bytes(s, dtype);
+    const DeltaWorkspace ws = delta_workspace(p, dtype);
+    const size_t ws_need = ws.total;
     if (ws_need > 0 && !workspace) return fail(SSD_ERR_WORKSPACE, "workspace is NULL");
     if (workspace_bytes < ws_need)
         return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, ws_need);
@@ -120,7 +138,11 @@ ssd_status ssd_gated_delta_fwd(const void *q, const void *k, const void *v, cons
     p.state_out_idx = state_out_idx;
     p.state_out = state_out;
     (void)hipGetLastError();  // start from a clean error state
-    return launched("gated_delta", ssd::launch_delta_tokens(p, elem(dtype), static_cast<hipStream_t>(hip_stream)));
+    const hipStream_t stream = static_cast<hipStream_t>(hip_stream);
+    if (p.nchunks == 0) return launched("gated_delta", ssd::launch_delta_tokens(p, elem(dtype), stream));
+    p.pack = static_cast<char *>(workspace);
+    p.at_tables = reinterpret_cast<float *>(p.pack + ws.at_off);
+    return launched("gated_delta", ssd::launch_delta_chunks(p, elem(dtype), stream));
 }
 
 ssd_status ssd_residual_norm_fwd(const void *x, const void *residual, const void *gate, int gate_activation,

@@ -1,0 +1,653 @@
+// Gated delta rule in chunks of 32 tokens, for prompts.
+//
+// With Gam_i the sum of g from the chunk's first token to token i, S the state
+// that enters the chunk and kr, qr the factors that normalise and scale keys and
+// queries, the chunk's updates u (S_t = ... + kr_t u_t k_t') solve
+//
+//     u_i + beta_i sum_{j<i} e^{Gam_i-Gam_j} kr_i kr_j (k_i.k_j) u_j
+//         = beta_i (v_i - e^{Gam_i} kr_i S k_i),
+//
+// so U = Tb X with Tb = (1 + A)^-1 diag(beta) and X_i = v_i - a_i S k_i, and
+//
+//     y_i = c_i S q_i + sum_{j<=i} Pm_ij u_j,  Pm_ij = qr_i kr_j e^{Gam_i-Gam_j} q_i.k_j
+//     S'  = e^{Gam_C} S + sum_j d_j u_j k_j',  a = e^{Gam} kr, c = e^{Gam} qr, d = e^{Gam_C-Gam} kr.
+//
+// Two launches.  delta_prepare takes a wave per (sequence, chunk, head), all of
+// them at once, and leaves Tb and Pm in the workspace in the order in which the
+// matrix cores read them, with the tables a, c, d.  delta_chunks walks the chunks
+// of a (sequence, head) in order.  There a wave owns 16 rows p of the state and
+// all of N, as S' tiles [n, p] in its accumulators: a result tile (rows 4 (l/16)
+// + r, column l%16 = p) is the next product's operand as it stands, so nothing
+// passes between waves and only the operands that they share (k, q, v, Tb, Pm)
+// go through LDS, one chunk ahead.
+//
+// States, X and U are fp32 and enter the products as sums of bf16 terms: three
+// hold all 24 bits of the fraction, and of the products of two such sums those
+// below 2^-24 of the first are left out.  bf16 inputs are one term, fp32 ones
+// three.  Where the result is only rounded to a bf16 output (S q and Pm U of bf16
+// calls), two terms (16 bits) are taken: 2^-16 beside the output's 2^-8.  This is
+// 3 to 6 products of the bf16 rate, which is 16 times the fp32 rate.
+#include "device_common.hpp"
+#include "kernels.hpp"
+
+namespace ssd {
+namespace {
+
+constexpr int C = kDeltaChunk;   // 32 tokens
+constexpr int kThreads = 256;    // four waves
+constexpr int kSlice = 64;       // rows of the state of a workgroup, 16 per wave
+constexpr float kNormEps = 1e-6f;
+
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2), may_alias));
+
+template <typename T> constexpr int kIn = sizeof(T) == 2 ? 1 : 3;   // terms of an input
+template <typename T> constexpr int kOut = sizeof(T) == 2 ? 2 : 3;  // terms of what an output is read from
+
+// What delta_prepare leaves per (sequence, head, chunk), in bytes: Tb by row
+// tile (the upper one needs the first 16 tokens only: half fragments) and term,
+// then Pm, then the tables.
+template <typename T>
+struct Pack32 {
+    static constexpr int kT0 = 0, kT1 = kT0 + 3 * 64 * 8, kP0 = kT1 + 3 * 64 * 16, kP1 = kP0 + kOut<T> * 64 * 8,
+                         kTab = kP1 + kOut<T> * 64 * 16, kBytes = kTab + 512;
+    // floats of the tables
+    static constexpr int kA = 0, kC = 32, kD = 64, kEnd = 96;
+};
+constexpr int kAtFloats = 36;  // the accepted index's weights [32] and decay, per (sequence, head)
+
+// 2^d for d in fp64: the whole part goes into the exponent, so the result is
+// off by the hardware exponential's unit however large d is.
+__device__ __forceinline__ float exp2_f64(double d) {
+    d = fmin(fmax(d, -1000.0), 1000.0);
+    const double n = rint(d);
+    return ldexpf(exp2_hw((float)(d - n)), (int)n);
+}
+
+__device__ __forceinline__ float bf16_f32(bf16 v) { return (float)v; }
+
+// v as a sum of N terms, each the next 8 bits (round to nearest even).
+template <int N>
+__device__ __forceinline__ void split8(const float (&v)[8], bf16x8 (&t)[N]) {
+    float rest[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = v[i];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[k][i] = (bf16)rest[i];
+        if (k + 1 < N)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) rest[i] -= bf16_f32(t[k][i]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void split4(const float (&v)[4], bf16x4 (&t)[N]) {
+    float rest[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rest[i] = v[i];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[k][i] = (bf16)rest[i];
+        if (k + 1 < N)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rest[i] -= bf16_f32(t[k][i]);
+    }
+}
+
+__device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, const f32x4 &c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(const bf16x4 &a, const bf16x4 &b, const f32x4 &c) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0, 0, 0);
+}
+// acc += (sum of a's terms) (sum of b's terms) without the products below the
+// last bit kept, the smallest first.
+template <int TA, int TB, typename V, int NA, int NB>
+__device__ __forceinline__ void mma_terms(const V (&a)[NA], const V (&b)[NB], f32x4 &acc) {
+    static_assert(TA <= NA && TB <= NB, "terms");
+    constexpr int K = TA > TB ? TA : TB;
+#pragma unroll
+    for (int s = K - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < TA; ++i)
+            if (s - i >= 0 && s - i < TB) acc = mfma(a[i], b[s - i], acc);
+}
+
+// ------------------------------------------------------------------ prepare
+template <typename T> __device__ __forceinline__ void load_frag(Frag<T> &f, const T *p, bool valid);
+template <> __device__ __forceinline__ void load_frag<bf16>(Frag<bf16> &f, const bf16 *p, bool valid) {
+    f.zero();
+    if (valid) f.v = __builtin_bit_cast(bf16x8, load_words(p));
+}
+template <> __device__ __forceinline__ void load_frag<float>(Frag<float> &f, const float *p, bool valid) {
+    f.zero();
+    if (valid) {
+        f.lo = __builtin_bit_cast(f32x4, load_words(p));
+        f.hi = __builtin_bit_cast(f32x4, load_words(p + 4));
+    }
+}
+__device__ __forceinline__ float squares(const Frag<bf16> &f, float s) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(bf16_f32(f.v[i]), bf16_f32(f.v[i]), s);
+    return s;
+}
+__device__ __forceinline__ float squares(const Frag<float> &f, float s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = fmaf(f.hi[i], f.hi[i], fmaf(f.lo[i], f.lo[i], s));
+    return s;
+}
+__device__ __forceinline__ f32x4 mma_f32_16(const f32x4 &a, const f32x4 &b, f32x4 acc) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], acc, 0, 0, 0);
+    return acc;
+}
+
+struct WaveTables {
+    double cs2[C];       // Gam_i log2 e
+    float beta[C], kr[C], qr[C];
+    float at[2][16][20];  // A's diagonal blocks, transposed: [j][m]; rows padded
+    float tb[2][16][20];  // their inverses, row-major
+};
+
+// A wave per (b, chunk, head).  Every 16 x 16 tile is computed transposed, so
+// that lane l holds row i = l%16 and columns j = 4 (l/16) + r: the layout in which
+// delta_chunks feeds it to the matrix cores.  The inverse takes the two diagonal
+// blocks by substitution (a lane per row: t_j = [j = i] - sum_{m>j} t_m A_mj) and
+// joins them, -T11 A10 T00, by fp32 products.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
+    __shared__ WaveTables tables[kThreads / 64];
+    WaveTables &w = tables[threadIdx.x >> 6];
+    const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
+    const int64_t items = p.batch * p.nchunks * p.nheads;
+    const int64_t mine = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6), item = min(mine, items - 1);
+    const int h = (int)(item % p.nheads);
+    const int64_t bc = item / p.nheads, b = bc / p.nchunks, c = bc - b * p.nchunks, t0 = c * C;
+    const int group = h / p.heads_per_group;
+
+    // Tables of the tokens, a lane each; past the end nothing is written
+    // (beta 0) and nothing decays.
+    double gam = 0.0;
+    float beta = 0.0f;
+    if (lane < C && t0 + lane < p.seqlen) {
+        if (p.g) gam = (double)p.g[b * p.g_bs + (t0 + lane) * p.g_ts + h] * 1.4426950408889634;
+        beta = p.beta[b * p.beta_bs + (t0 + lane) * p.beta_ts + h];
+    }
+#pragma unroll
+    for (int m = 1; m < C; m <<= 1) {
+        const double o = __shfl_up(gam, m);
+        if (lane >= m) gam += o;
+    }
+    if (lane < C) {
+        w.cs2[lane] = gam;
+        w.beta[lane] = beta;
+    }
+
+    // Products of keys with keys and queries: tile (I, J) = lanes (i in I, j in J).
+    const T *kbase = reinterpret_cast<const T *>(p.k) + b * p.k_bs + (int64_t)group * p.dstate;
+    const T *qbase = reinterpret_cast<const T *>(p.q) + b * p.q_bs + (int64_t)group * p.dstate;
+    const T *krow[2], *qrow[2];
+#pragma unroll
+    for (int I = 0; I < 2; ++I) {
+        const int64_t t = min(t0 + 16 * I + i16, p.seqlen - 1);
+        krow[I] = kbase + t * p.k_ts;
+        qrow[I] = qbase + t * p.q_ts;
+    }
+    f32x4 kk[3] = {}, qk[3] = {};  // tiles 00, 10, 11
+    float ksq[2] = {0.f, 0.f}, qsq[2] = {0.f, 0.f};
+    for (int n = 8 * g; n - 8 * g < p.dstate; n += 32) {
+        Frag<T> k[2], q[2];
+#pragma unroll
+        for (int I = 0; I < 2; ++I) {
+            load_frag<T>(k[I], krow[I] + n, n < p.dstate);
+            load_frag<T>(q[I], qrow[I] + n, n < p.dstate);
+        }
+#pragma unroll
+        for (int I = 0; I < 2; ++I) {
+            ksq[I] = squares(k[I], ksq[I]);
+            qsq[I] = squares(q[I], qsq[I]);
+        }
+        mma(k[0], k[0], kk[0]);
+        mma(k[0], k[1], kk[1]);
+        mma(k[1], k[1], kk[2]);
+        mma(k[0], q[0], qk[0]);
+        mma(k[0], q[1], qk[1]);
+        mma(k[1], q[1], qk[2]);
+    }
+#pragma unroll
+    for (int I = 0; I < 2; ++I) {
+#pragma unroll
+        for (int m = 16; m < 64; m <<= 1) {
+            ksq[I] += __shfl_xor(ksq[I], m);
+            qsq[I] += __shfl_xor(qsq[I], m);
+        }
+        if (g == 0) {
+            w.kr[16 * I + i16] = p.l2norm ? 1.0f / sqrtf(ksq[I] + kNormEps) : 1.0f;
+            w.qr[16 * I + i16] = p.l2norm ? p.scale * (1.0f / sqrtf(qsq[I] + kNormEps)) : p.scale;
+        }
+    }
+    __syncthreads();
+
+    // A and Pm.
+    float pm[3][4];
+    f32x4 a10;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int I = (k + 1) / 2, J = k / 2, i = 16 * I + i16;
+        const double ci = w.cs2[i];
+        const float bi = w.beta[i] * w.kr[i], qi = w.qr[i];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int j = 16 * J + 4 * g + r;
+            const float e = exp2_f64(ci - w.cs2[j]) * w.kr[j];
+            pm[k][r] = j <= i ? qi * e * qk[k][r] : 0.0f;
+            const float a = j < i ? bi * e * kk[k][r] : 0.0f;
+            if (k == 1) a10[r] = a;
+            else w.at[I][4 * g + r][i16] = a;
+        }
+    }
+    __syncthreads();
+    {
+        const int blk = g & 1;
+        float t[16];
+#pragma unroll
+        for (int j = 15; j >= 0; --j) {
+            float s = 0.0f;
+#pragma unroll
+            for (int m = 15; m > j; --m) s = fmaf(t[m], w.at[blk][j][m], s);
+            t[j] = (j == i16 ? 1.0f : 0.0f) - s;
+        }
+        if (g < 2)
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<f32x4 *>(&w.tb[blk][i16][j]) = f32x4{t[j], t[j + 1], t[j + 2], t[j + 3]};
+    }
+    __syncthreads();
+    f32x4 tt[3];
+    tt[0] = *reinterpret_cast<const f32x4 *>(&w.tb[0][i16][4 * g]);
+    tt[2] = *reinterpret_cast<const f32x4 *>(&w.tb[1][i16][4 * g]);
+    f32x4 t00t;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) t00t[r] = w.tb[0][4 * g + r][i16];
+    const f32x4 prod = mma_f32_16(a10, t00t, f32x4{0.f, 0.f, 0.f, 0.f});  // (A10 T00)[m][j]: lane j, rows m
+    const f32x4 joined = mma_f32_16(prod, tt[2], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+    for (int r = 0; r < 4; ++r) tt[1][r] = -joined[r];
+
+    if (mine >= items) return;
+    typedef Pack32<T> L;
+    char *out = p.pack + ((b * p.nheads + h) * p.nchunks + c) * L::kBytes;
+    float tv[3][4];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) tv[k][r] = tt[k][r] * w.beta[16 * (k / 2) + 4 * g + r];
+    auto put = [&](const float (&lo)[4], const float (&hi)[4], int off, auto terms) {
+        constexpr int N = decltype(terms)::value;
+        const float both[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        bf16x8 f[N];
+        split8(both, f);
+#pragma unroll
+        for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x8 *>(out + off + (k * 64 + lane) * 16) = f[k];
+    };
+    auto put_half = [&](const float (&v)[4], int off, auto terms) {
+        constexpr int N = decltype(terms)::value;
+        bf16x4 f[N];
+        split4(v, f);
+#pragma unroll
+        for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x4 *>(out + off + (k * 64 + lane) * 8) = f[k];
+    };
+    put_half(tv[0], L::kT0, std::integral_constant<int, 3>{});
+    put(tv[1], tv[2], L::kT1, std::integral_constant<int, 3>{});
+    put_half(pm[0], L::kP0, std::integral_constant<int, kOut<T>>{});
+    put(pm[1], pm[2], L::kP1, std::integral_constant<int, kOut<T>>{});
+    float *tab = reinterpret_cast<float *>(out + L::kTab);
+    if (lane < C) {
+        const double cs = w.cs2[lane], end = w.cs2[C - 1];
+        const float e = exp2_f64(cs);
+        tab[L::kA + lane] = e * w.kr[lane];
+        tab[L::kC + lane] = e * w.qr[lane];
+        tab[L::kD + lane] = exp2_f64(end - cs) * w.kr[lane];
+        if (lane == 0) tab[L::kEnd] = exp2_f64(end);
+    }
+    if (p.state_out) {
+        const int64_t at = min(max((int64_t)p.state_out_idx[b], (int64_t)-1), p.seqlen - 1);
+        if (at >= t0 && at < t0 + C && lane < C) {
+            float *to = p.at_tables + (b * p.nheads + h) * kAtFloats;
+            const double ce = w.cs2[(int)(at - t0)];
+            to[lane] = lane <= (int)(at - t0) ? exp2_f64(ce - w.cs2[lane]) * w.kr[lane] : 0.0f;
+            if (lane == 0) to[C] = exp2_f64(ce);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- chunks
+template <typename T, int NB>
+struct Buffer {
+    static constexpr int kPlane = 32 * NB + 16;  // elements of a row of keys or queries, padded by 32 bytes
+    static constexpr int kVRow = kSlice + 32 / (int)sizeof(T);
+    alignas(16) bf16 k[kIn<T>][C][kPlane];
+    alignas(16) bf16 q[kIn<T>][C][kPlane];
+    alignas(16) T v[C][kVRow];
+    alignas(16) char pack[Pack32<T>::kBytes];
+};
+
+// What a thread carries from global memory to LDS, one chunk ahead.
+template <typename T, int NB>
+struct Carry {
+    static constexpr int VEC = 16 / sizeof(T), WORDS = 8 / VEC;  // 16-byte words of 8 elements
+    static constexpr int kPackWords = (Pack32<T>::kBytes / 16 + kThreads - 1) / kThreads;
+    u32x4 kq[NB][WORDS], v[WORDS], pack[kPackWords];
+};
+
+template <typename T, int NB, int BUFS>
+__global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
+    typedef Pack32<T> L;
+    typedef Buffer<T, NB> Buf;
+    typedef Carry<T, NB> Regs;
+    constexpr int NI = kIn<T>, NO = kOut<T>;
+    __shared__ Buf bufs[BUFS];
+
+    // Consecutive items (the slices of a head, the heads of a group) on one XCD.
+    const unsigned xcd = blockIdx.x % 8, whole = gridDim.x / 8, more = gridDim.x % 8;
+    const unsigned item = xcd * whole + min(xcd, more) + blockIdx.x / 8;
+    const int slices = (p.headdim + kSlice - 1) / kSlice;
+    const unsigned bh = item / (unsigned)slices, b = bh / (unsigned)p.nheads, h = bh - b * (unsigned)p.nheads;
+    const int slice0 = (int)(item - bh * (unsigned)slices) * kSlice;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, g = lane >> 4;
+    const int N = p.dstate, p0 = slice0 + 16 * wave;
+    const bool live = p0 < p.headdim;  // whole waves only: headdim is a multiple of 16
+    const int group = (int)h / p.heads_per_group;
+
+    const T *kbase = reinterpret_cast<const T *>(p.k) + b * p.k_bs + (int64_t)group * N;
+    const T *qbase = reinterpret_cast<const T *>(p.q) + b * p.q_bs + (int64_t)group * N;
+    const T *vbase = reinterpret_cast<const T *>(p.v) + b * p.v_bs + (int64_t)h * p.headdim + slice0;
+    const char *packs = p.pack + (int64_t)bh * p.nchunks * L::kBytes;
+    const u32x4 none = {0u, 0u, 0u, 0u};
+
+    // Eight elements per piece; rows past the end repeat the last one (their u
+    // are 0), columns past N are 0.
+    auto fetch = [&](Regs &r, int64_t c) {
+        const int64_t t0 = c * C;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int at = tid + kThreads * i, is_q = at >= 128 * NB, piece = is_q ? at - 128 * NB : at;
+            const int row = piece / (4 * NB), n = 8 * (piece % (4 * NB));
+            const int64_t t = min(t0 + row, p.seqlen - 1);
+            const T *src = (is_q ? qbase + t * p.q_ts : kbase + t * p.k_ts) + n;
+#pragma unroll
+            for (int j = 0; j < Regs::WORDS; ++j) {
+                r.kq[i][j] = none;
+                if (n < N) r.kq[i][j] = load_words(src + j * Regs::VEC);
+            }
+        }
+        {
+            const int row = tid >> 3, n = 8 * (tid & 7);
+            const T *src = vbase + min(t0 + row, p.seqlen - 1) * p.v_ts + n;
+#pragma unroll
+            for (int j = 0; j < Regs::WORDS; ++j) {
+                r.v[j] = none;
+                if (slice0 + n < p.headdim) r.v[j] = load_words(src + j * Regs::VEC);
+            }
+        }
+        const u32x4 *src = reinterpret_cast<const u32x4 *>(packs + c * L::kBytes);
+#pragma unroll
+        for (int i = 0; i < Regs::kPackWords; ++i) r.pack[i] = src[min(tid + kThreads * i, L::kBytes / 16 - 1)];
+    };
+    auto place = [&](const Regs &r, Buf &to) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int at = tid + kThreads * i, is_q = at >= 128 * NB, piece = is_q ? at - 128 * NB : at;
+            const int row = piece / (4 * NB), n = 8 * (piece % (4 * NB));
+            if constexpr (NI == 1) {
+                *reinterpret_cast<u32x4 *>(is_q ? &to.q[0][row][n] : &to.k[0][row][n]) = r.kq[i][0];
+            } else {
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = word_f32(r.kq[i][e / 4], e % 4, float());
+                bf16x8 t[3];
+                split8(f, t);
+#pragma unroll
+                for (int e = 0; e < NI; ++e) *reinterpret_cast<bf16x8 *>(is_q ? &to.q[e][row][n] : &to.k[e][row][n]) = t[e];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < Regs::WORDS; ++j)
+            *reinterpret_cast<u32x4 *>(&to.v[tid >> 3][8 * (tid & 7) + j * Regs::VEC]) = r.v[j];
+#pragma unroll
+        for (int i = 0; i < Regs::kPackWords; ++i)
+            if (tid + kThreads * i < L::kBytes / 16) *reinterpret_cast<u32x4 *>(to.pack + 16 * (tid + kThreads * i)) = r.pack[i];
+    };
+
+    // Tile (kb, half) of the state: rows n = 32 kb + 8 g + 4 half + r, column p0 +
+    // i16; the two halves' eight rows of a lane are consecutive.
+    f32x4 s[NB][2];
+    const int64_t s_off = ((int64_t)bh * p.headdim + (live ? p0 : 0) + i16) * N + 8 * g;
+    auto store_state = [&](const f32x4 (&m)[NB][2], float *to) {
+        if (!live) return;
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+            if (32 * kb + 8 * g < N) {
+                *reinterpret_cast<f32x4 *>(to + s_off + 32 * kb) = m[kb][0];
+                *reinterpret_cast<f32x4 *>(to + s_off + 32 * kb + 4) = m[kb][1];
+            }
+    };
+#pragma unroll
+    for (int kb = 0; kb < NB; ++kb) {
+        s[kb][0] = s[kb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (p.init_state && 32 * kb + 8 * g < N) {
+            s[kb][0] = *reinterpret_cast<const f32x4 *>(p.init_state + s_off + 32 * kb);
+            s[kb][1] = *reinterpret_cast<const f32x4 *>(p.init_state + s_off + 32 * kb + 4);
+        }
+    }
+    int64_t at = -2;  // the accepted index
+    if (p.state_out) {
+        at = min(max((int64_t)p.state_out_idx[b], (int64_t)-1), p.seqlen - 1);
+        if (at < 0) store_state(s, p.state_out);
+    }
+
+    // K' of a chunk as an operand with rows n of tile (kb, half) and the tokens
+    // 4 g + r of both token tiles as the contraction.
+    auto keys_t = [&](const Buf &buf, int kb, int half, bf16x8 (&f)[NI]) {
+#pragma unroll
+        for (int e = 0; e < NI; ++e) {
+            const bf16 *src = &buf.k[e][4 * g + (i16 >> 2)][32 * kb + 8 * (i16 & 3) + 4 * half];
+            const i16x4 lo = ds_read_tr16(src), hi = ds_read_tr16(src + 16 * Buf::kPlane);
+            typedef short i16x8 __attribute__((ext_vector_type(8)));
+            f[e] = __builtin_bit_cast(bf16x8, (i16x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        }
+    };
+
+    Regs regs;
+    fetch(regs, 0);
+    place(regs, bufs[0]);
+    __syncthreads();
+    const int64_t nc = p.nchunks;
+    for (int64_t c = 0; c < nc; ++c) {
+        const Buf &buf = bufs[BUFS == 2 ? (int)(c & 1) : 0];
+        if (c + 1 < nc) fetch(regs, c + 1);
+        if (live) {
+            const float *tab = reinterpret_cast<const float *>(buf.pack + L::kTab);
+            // S k (rows: tokens) and S q (rows: p).
+            f32x4 ks[2] = {}, qs[2] = {};
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = s[kb][i >> 2][i & 3];
+                bf16x8 sf[3];
+                split8(f, sf);
+#pragma unroll
+                for (int I = 0; I < 2; ++I) {
+                    bf16x8 kf[NI], qf[NI];
+#pragma unroll
+                    for (int e = 0; e < NI; ++e) {
+                        kf[e] = *reinterpret_cast<const bf16x8 *>(&buf.k[e][16 * I + i16][32 * kb + 8 * g]);
+                        qf[e] = *reinterpret_cast<const bf16x8 *>(&buf.q[e][16 * I + i16][32 * kb + 8 * g]);
+                    }
+                    mma_terms<NI, 3>(kf, sf, ks[I]);
+                    mma_terms<NO, NI>(sf, qf, qs[I]);
+                }
+            }
+            // X = v - a S k, then U = Tb X.
+            float x[8];
+#pragma unroll
+            for (int I = 0; I < 2; ++I) {
+                const f32x4 a = *reinterpret_cast<const f32x4 *>(tab + L::kA + 16 * I + 4 * g);
+                float v[4];
+                if constexpr (sizeof(T) == 2) {
+                    const i16x4 t = ds_read_tr16(&buf.v[16 * I + 4 * g + (i16 >> 2)][16 * wave + 4 * (i16 & 3)]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        v[r] = __builtin_bit_cast(float, (uint32_t)(uint16_t)t[r] << 16);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = buf.v[16 * I + 4 * g + r][16 * wave + i16];
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[4 * I + r] = fmaf(-a[r], ks[I][r], v[r]);
+            }
+            bf16x8 xf[3];
+            split8(x, xf);
+            f32x4 u[2] = {};
+            {
+                bf16x4 t0[3], x0[3];
+                bf16x8 t1[3];
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    t0[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + L::kT0 + (e * 64 + lane) * 8);
+                    t1[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + L::kT1 + (e * 64 + lane) * 16);
+                    x0[e] = bf16x4{xf[e][0], xf[e][1], xf[e][2], xf[e][3]};
+                }
+                mma_terms<3, 3>(t0, x0, u[0]);
+                mma_terms<3, 3>(t1, xf, u[1]);
+            }
+            // y: rows p = p0 + 4 g + r, column: token 16 I + i16.
+            {
+                float uv[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3];
+                bf16x8 uf[NO], p1[NO];
+                bf16x4 u0[NO], pm0[NO];
+                split8(uv, uf);
+#pragma unroll
+                for (int e = 0; e < NO; ++e) {
+                    u0[e] = bf16x4{uf[e][0], uf[e][1], uf[e][2], uf[e][3]};
+                    pm0[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + L::kP0 + (e * 64 + lane) * 8);
+                    p1[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + L::kP1 + (e * 64 + lane) * 16);
+                }
+#pragma unroll
+                for (int I = 0; I < 2; ++I) {
+                    const float ci = tab[L::kC + 16 * I + i16];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) qs[I][r] *= ci;
+                }
+                mma_terms<NO, NO>(u0, pm0, qs[0]);
+                mma_terms<NO, NO>(uf, p1, qs[1]);
+#pragma unroll
+                for (int I = 0; I < 2; ++I) {
+                    const int64_t t = c * C + 16 * I + i16;
+                    T *to = reinterpret_cast<T *>(p.y) + (((int64_t)b * p.seqlen + t) * p.nheads + h) * p.headdim + p0 + 4 * g;
+                    if (t < p.seqlen) {
+                        if constexpr (sizeof(T) == 2) {
+                            const bf16x4 o = {(bf16)qs[I][0], (bf16)qs[I][1], (bf16)qs[I][2], (bf16)qs[I][3]};
+                            *reinterpret_cast<u32x2_at2 *>(to) = __builtin_bit_cast(u32x2, o);
+                        } else {
+                            store_words(to, __builtin_bit_cast(u32x4, qs[I]));
+                        }
+                    }
+                }
+            }
+            // The state after the accepted index, then after the chunk.
+            if (at >= c * C && at < c * C + C) {
+                const float *wt = p.at_tables + (int64_t)bh * kAtFloats;
+                const float e = wt[C];
+                float uv[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3] * wt[16 * (i >> 2) + 4 * g + (i & 3)];
+                bf16x8 uf[3];
+                split8(uv, uf);
+                f32x4 m[NB][2];
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        bf16x8 kf[NI];
+                        keys_t(buf, kb, half, kf);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) m[kb][half][r] = s[kb][half][r] * e;
+                        mma_terms<NI, 3>(kf, uf, m[kb][half]);
+                    }
+                store_state(m, p.state_out);
+            }
+            {
+                const float e = tab[L::kEnd];
+                float uv[8];
+#pragma unroll
+                for (int I = 0; I < 2; ++I) {
+                    const f32x4 d = *reinterpret_cast<const f32x4 *>(tab + L::kD + 16 * I + 4 * g);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) uv[4 * I + r] = u[I][r] * d[r];
+                }
+                bf16x8 uf[3];
+                split8(uv, uf);
+#pragma unroll
+                for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        bf16x8 kf[NI];
+                        keys_t(buf, kb, half, kf);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) s[kb][half][r] *= e;
+                        mma_terms<NI, 3>(kf, uf, s[kb][half]);
+                    }
+            }
+        }
+        if (BUFS == 1) __syncthreads();  // the only buffer is read no more
+        if (c + 1 < nc) place(regs, bufs[BUFS == 2 ? (int)((c + 1) & 1) : 0]);
+        __syncthreads();
+    }
+    if (p.final_state) store_state(s, p.final_state);
+}
+
+template <typename T, int NB>
+hipError_t launch_chunks(const DeltaParams &p, hipStream_t stream) {
+    constexpr int kLds = 160 * 1024;
+    constexpr int BUFS = 2 * sizeof(Buffer<T, NB>) <= kLds ? 2 : 1;
+    static_assert(BUFS * sizeof(Buffer<T, NB>) <= kLds, "LDS");
+    const int64_t items = p.batch * p.nheads * ((p.headdim + kSlice - 1) / kSlice);
+    delta_chunks<T, NB, BUFS><<<(unsigned)items, kThreads, 0, stream>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run(const DeltaParams &p, hipStream_t stream) {
+    const int64_t waves = p.batch * p.nchunks * p.nheads;
+    delta_prepare<T><<<(unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
+    const hipError_t r = hipGetLastError();
+    if (r != hipSuccess) return r;
+    switch ((p.dstate + 31) / 32) {
+        case 1: return launch_chunks<T, 1>(p, stream);
+        case 2: return launch_chunks<T, 2>(p, stream);
+        case 3: return launch_chunks<T, 3>(p, stream);
+        case 4: return launch_chunks<T, 4>(p, stream);
+        case 5: return launch_chunks<T, 5>(p, stream);
+        case 6: return launch_chunks<T, 6>(p, stream);
+        case 7: return launch_chunks<T, 7>(p, stream);
+        default: return launch_chunks<T, 8>(p, stream);
+    }
+}
+
+}  // namespace
+
+size_t delta_pack_bytes(Elem e) { return e == Elem::BF16 ? Pack32<bf16>::kBytes : Pack32<float>::kBytes; }
+size_t delta_at_bytes() { return kAtFloats * sizeof(float); }
+
+hipError_t launch_delta_chunks(const DeltaParams &p, Elem e, hipStream_t stream) {
+    return e == Elem::BF16 ? run<bf16>(p, stream) : run<float>(p, stream);
+}
+
+}  // namespace ssd

@@ -149,8 +149,18 @@ struct DeltaParams {
     int nheads, headdim, dstate, ngroups, heads_per_group;
     float scale;
     int l2norm;
+    // Chunked form only, in the workspace: delta_pack_bytes per (b, h, chunk) and
+    // delta_at_bytes per (b, h).
+    int64_t nchunks;
+    char *pack;
+    float *at_tables;
 };
+constexpr int kDeltaChunk = 32;  // tokens of a chunk
+// Token by token (any number of them), and in chunks with the workspace.
 hipError_t launch_delta_tokens(const DeltaParams &p, Elem e, hipStream_t stream);
+hipError_t launch_delta_chunks(const DeltaParams &p, Elem e, hipStream_t stream);
+size_t delta_pack_bytes(Elem e);
+size_t delta_at_bytes();
 
 // Norms before and after a block (ssd_residual_norm_fwd).
 struct ResidualNormParams {
