@@ -66,34 +66,29 @@ __device__ __forceinline__ float exp2_f64(double d) {
 
 __device__ __forceinline__ float bf16_f32(bf16 v) { return (float)v; }
 
-// v as a sum of N terms, each the next 8 bits (round to nearest even).
-template <int N>
-__device__ __forceinline__ void split8(const float (&v)[8], bf16x8 (&t)[N]) {
-    float rest[8];
+// v as a sum of N bf16 terms, each the next 8 bits of the fraction (cut off, so
+// that three terms are v itself and two leave less than 2^-15 of it).  A pair of
+// values takes one byte permutation per term and an and and a subtraction per
+// value between terms; rounding with v_cvt_pk_bf16_f32 costs as many and half of
+// them at twice the time.
+template <int N, int LEN, typename V>
+__device__ __forceinline__ void split(const float (&v)[LEN], V (&t)[N]) {
+    uint32_t w[N][LEN / 2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rest[i] = v[i];
+    for (int i = 0; i < LEN; i += 2) {
+        float lo = v[i], hi = v[i + 1];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[k][i] = (bf16)rest[i];
-        if (k + 1 < N)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) rest[i] -= bf16_f32(t[k][i]);
+        for (int k = 0; k < N; ++k) {
+            const uint32_t l = __builtin_bit_cast(uint32_t, lo), h = __builtin_bit_cast(uint32_t, hi);
+            w[k][i / 2] = __builtin_amdgcn_perm(h, l, 0x07060302u);
+            if (k + 1 < N) {
+                lo -= __builtin_bit_cast(float, l & 0xffff0000u);
+                hi -= __builtin_bit_cast(float, h & 0xffff0000u);
+            }
+        }
     }
-}
-template <int N>
-__device__ __forceinline__ void split4(const float (&v)[4], bf16x4 (&t)[N]) {
-    float rest[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rest[i] = v[i];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[k][i] = (bf16)rest[i];
-        if (k + 1 < N)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rest[i] -= bf16_f32(t[k][i]);
-    }
+    for (int k = 0; k < N; ++k) __builtin_memcpy(&t[k], w[k], sizeof(V));
 }
 
 __device__ __forceinline__ f32x4 mfma(const bf16x8 &a, const bf16x8 &b, const f32x4 &c) {
@@ -289,14 +284,14 @@ __global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
         constexpr int N = decltype(terms)::value;
         const float both[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         bf16x8 f[N];
-        split8(both, f);
+        split(both, f);
 #pragma unroll
         for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x8 *>(out + off + (k * 64 + lane) * 16) = f[k];
     };
     auto put_half = [&](const float (&v)[4], int off, auto terms) {
         constexpr int N = decltype(terms)::value;
         bf16x4 f[N];
-        split4(v, f);
+        split(v, f);
 #pragma unroll
         for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x4 *>(out + off + (k * 64 + lane) * 8) = f[k];
     };
@@ -343,8 +338,10 @@ struct Carry {
     u32x4 kq[NB][WORDS], v[WORDS], pack[kPackWords];
 };
 
-template <typename T, int NB, int BUFS>
-__global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
+// WAVES: waves per SIMD to leave registers for (two keep the accumulators in
+// the ordinary registers too).
+template <typename T, int NB, int BUFS, int WAVES>
+__global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     typedef Pack32<T> L;
     typedef Buffer<T, NB> Buf;
     typedef Carry<T, NB> Regs;
@@ -366,42 +363,67 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
     const T *qbase = reinterpret_cast<const T *>(p.q) + b * p.q_bs + (int64_t)group * N;
     const T *vbase = reinterpret_cast<const T *>(p.v) + b * p.v_bs + (int64_t)h * p.headdim + slice0;
     const char *packs = p.pack + (int64_t)bh * p.nchunks * L::kBytes;
-    const u32x4 none = {0u, 0u, 0u, 0u};
-
     // Eight elements per piece; rows past the end repeat the last one (their u
-    // are 0), columns past N are 0.
-    auto fetch = [&](Regs &r, int64_t c) {
-        const int64_t t0 = c * C;
+    // are 0), columns past N are 0.  A thread's pieces keep their rows and
+    // columns, so their addresses only move on by a chunk; the last chunk's may
+    // be cut short, which `cut` sees to.
+    const T *kq_at[NB], *v_at;
+    const int v_row = tid >> 3, v_col = 8 * (tid & 7);
+    auto piece_of = [&](int i, bool &is_q, int &row, int &n) {
+        const int at = tid + kThreads * i;
+        is_q = at >= 128 * NB;
+        const int piece = is_q ? at - 128 * NB : at;
+        row = piece / (4 * NB);
+        n = 8 * (piece % (4 * NB));
+    };
+    auto point = [&](int64_t c) {
+        const int left = (int)min(p.seqlen - c * C, (int64_t)C) - 1;  // the last row
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int at = tid + kThreads * i, is_q = at >= 128 * NB, piece = is_q ? at - 128 * NB : at;
-            const int row = piece / (4 * NB), n = 8 * (piece % (4 * NB));
-            const int64_t t = min(t0 + row, p.seqlen - 1);
-            const T *src = (is_q ? qbase + t * p.q_ts : kbase + t * p.k_ts) + n;
-#pragma unroll
-            for (int j = 0; j < Regs::WORDS; ++j) {
-                r.kq[i][j] = none;
-                if (n < N) r.kq[i][j] = load_words(src + j * Regs::VEC);
-            }
+            bool is_q;
+            int row, n;
+            piece_of(i, is_q, row, n);
+            const int64_t t = c * C + min(row, left);
+            kq_at[i] = (is_q ? qbase + t * p.q_ts : kbase + t * p.k_ts) + min(n, N - 8);
         }
-        {
-            const int row = tid >> 3, n = 8 * (tid & 7);
-            const T *src = vbase + min(t0 + row, p.seqlen - 1) * p.v_ts + n;
+        v_at = vbase + (c * C + min(v_row, left)) * p.v_ts + min(v_col, p.headdim - slice0 - 8);
+    };
+    auto fetch = [&](Regs &r, int64_t c) {
+        if (c + 1 == p.nchunks && c > 0) point(c);
 #pragma unroll
-            for (int j = 0; j < Regs::WORDS; ++j) {
-                r.v[j] = none;
-                if (slice0 + n < p.headdim) r.v[j] = load_words(src + j * Regs::VEC);
-            }
+        for (int i = 0; i < NB; ++i) {
+#pragma unroll
+            for (int j = 0; j < Regs::WORDS; ++j) r.kq[i][j] = load_words(kq_at[i] + j * Regs::VEC);
+            bool is_q;
+            int row, n;
+            piece_of(i, is_q, row, n);
+            kq_at[i] += C * (is_q ? p.q_ts : p.k_ts);
         }
-        const u32x4 *src = reinterpret_cast<const u32x4 *>(packs + c * L::kBytes);
 #pragma unroll
-        for (int i = 0; i < Regs::kPackWords; ++i) r.pack[i] = src[min(tid + kThreads * i, L::kBytes / 16 - 1)];
+        for (int j = 0; j < Regs::WORDS; ++j) r.v[j] = load_words(v_at + j * Regs::VEC);
+        v_at += C * p.v_ts;
+        const char *src = packs + c * L::kBytes;
+        if constexpr (BUFS == 2) {
+            // The other buffer's last reader is behind the last barrier.
+            char *to = bufs[c & 1].pack;
+#pragma unroll
+            for (int i = 0; i < Regs::kPackWords; ++i) {
+                const int at = 16 * (kThreads * i + 64 * wave);
+                if (at + 1024 <= L::kBytes || at + 16 * lane < L::kBytes) copy16_to_lds(src + at + 16 * lane, to + at);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < Regs::kPackWords; ++i)
+                r.pack[i] = reinterpret_cast<const u32x4 *>(src)[min(tid + kThreads * i, L::kBytes / 16 - 1)];
+        }
     };
     auto place = [&](const Regs &r, Buf &to) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-            const int at = tid + kThreads * i, is_q = at >= 128 * NB, piece = is_q ? at - 128 * NB : at;
-            const int row = piece / (4 * NB), n = 8 * (piece % (4 * NB));
+            bool is_q;
+            int row, n;
+            piece_of(i, is_q, row, n);
+            if (n >= N) continue;
             if constexpr (NI == 1) {
                 *reinterpret_cast<u32x4 *>(is_q ? &to.q[0][row][n] : &to.k[0][row][n]) = r.kq[i][0];
             } else {
@@ -409,7 +431,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[e] = word_f32(r.kq[i][e / 4], e % 4, float());
                 bf16x8 t[3];
-                split8(f, t);
+                split(f, t);
 #pragma unroll
                 for (int e = 0; e < NI; ++e) *reinterpret_cast<bf16x8 *>(is_q ? &to.q[e][row][n] : &to.k[e][row][n]) = t[e];
             }
@@ -417,9 +439,10 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
 #pragma unroll
         for (int j = 0; j < Regs::WORDS; ++j)
             *reinterpret_cast<u32x4 *>(&to.v[tid >> 3][8 * (tid & 7) + j * Regs::VEC]) = r.v[j];
+        if constexpr (BUFS == 1)
 #pragma unroll
-        for (int i = 0; i < Regs::kPackWords; ++i)
-            if (tid + kThreads * i < L::kBytes / 16) *reinterpret_cast<u32x4 *>(to.pack + 16 * (tid + kThreads * i)) = r.pack[i];
+            for (int i = 0; i < Regs::kPackWords; ++i)
+                if (tid + kThreads * i < L::kBytes / 16) *reinterpret_cast<u32x4 *>(to.pack + 16 * (tid + kThreads * i)) = r.pack[i];
     };
 
     // Tile (kb, half) of the state: rows n = 32 kb + 8 g + 4 half + r, column p0 +
@@ -461,9 +484,15 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
         }
     };
 
+    if (N < 32 * NB) {  // columns that no piece fills
+        for (int i = tid; i < (int)sizeof(bufs) / 16; i += kThreads) reinterpret_cast<u32x4 *>(&bufs[0])[i] = u32x4{0u, 0u, 0u, 0u};
+        __syncthreads();
+    }
     Regs regs;
+    point(0);
     fetch(regs, 0);
     place(regs, bufs[0]);
+    wait_vmcnt<0>();
     __syncthreads();
     const int64_t nc = p.nchunks;
     for (int64_t c = 0; c < nc; ++c) {
@@ -479,7 +508,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = s[kb][i >> 2][i & 3];
                 bf16x8 sf[3];
-                split8(f, sf);
+                split(f, sf);
 #pragma unroll
                 for (int I = 0; I < 2; ++I) {
                     bf16x8 kf[NI], qf[NI];
@@ -511,7 +540,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
                 for (int r = 0; r < 4; ++r) x[4 * I + r] = fmaf(-a[r], ks[I][r], v[r]);
             }
             bf16x8 xf[3];
-            split8(x, xf);
+            split(x, xf);
             f32x4 u[2] = {};
             {
                 bf16x4 t0[3], x0[3];
@@ -532,7 +561,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
                 for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3];
                 bf16x8 uf[NO], p1[NO];
                 bf16x4 u0[NO], pm0[NO];
-                split8(uv, uf);
+                split(uv, uf);
 #pragma unroll
                 for (int e = 0; e < NO; ++e) {
                     u0[e] = bf16x4{uf[e][0], uf[e][1], uf[e][2], uf[e][3]};
@@ -569,7 +598,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3] * wt[16 * (i >> 2) + 4 * g + (i & 3)];
                 bf16x8 uf[3];
-                split8(uv, uf);
+                split(uv, uf);
                 f32x4 m[NB][2];
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb)
@@ -593,7 +622,7 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
                     for (int r = 0; r < 4; ++r) uv[4 * I + r] = u[I][r] * d[r];
                 }
                 bf16x8 uf[3];
-                split8(uv, uf);
+                split(uv, uf);
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
@@ -606,7 +635,8 @@ __global__ __launch_bounds__(kThreads) void delta_chunks(DeltaParams p) {
                     }
             }
         }
-        if (BUFS == 1) __syncthreads();  // the only buffer is read no more
+        if (BUFS == 2) wait_vmcnt<0>();  // the copies into the other buffer
+        else __syncthreads();            // the only buffer is read no more
         if (c + 1 < nc) place(regs, bufs[BUFS == 2 ? (int)((c + 1) & 1) : 0]);
         __syncthreads();
     }
@@ -619,7 +649,8 @@ hipError_t launch_chunks(const DeltaParams &p, hipStream_t stream) {
     constexpr int BUFS = 2 * sizeof(Buffer<T, NB>) <= kLds ? 2 : 1;
     static_assert(BUFS * sizeof(Buffer<T, NB>) <= kLds, "LDS");
     const int64_t items = p.batch * p.nheads * ((p.headdim + kSlice - 1) / kSlice);
-    delta_chunks<T, NB, BUFS><<<(unsigned)items, kThreads, 0, stream>>>(p);
+    constexpr int WAVES = 2 * BUFS * sizeof(Buffer<T, NB>) <= kLds && NB <= 5 ? 2 : 1;
+    delta_chunks<T, NB, BUFS, WAVES><<<(unsigned)items, kThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
