@@ -339,13 +339,16 @@ struct Carry {
 };
 
 // WAVES: waves per SIMD to leave registers for (two keep the accumulators in
-// the ordinary registers too).
-template <typename T, int NB, int BUFS, int WAVES>
+// the ordinary registers too).  DIRECT: bf16 rows of 16-byte alignment, which the
+// buffer loads that write LDS by themselves take; other rows pass through
+// registers.
+template <typename T, int NB, int BUFS, int WAVES, bool DIRECT>
 __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     typedef Pack32<T> L;
     typedef Buffer<T, NB> Buf;
     typedef Carry<T, NB> Regs;
     constexpr int NI = kIn<T>, NO = kOut<T>;
+    static_assert(!DIRECT || (sizeof(T) == 2 && BUFS == 2 && L::kBytes == 8 * 1024), "direct copies");
     __shared__ Buf bufs[BUFS];
 
     // Consecutive items (the slices of a head, the heads of a group) on one XCD.
@@ -363,10 +366,57 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     const T *qbase = reinterpret_cast<const T *>(p.q) + b * p.q_bs + (int64_t)group * N;
     const T *vbase = reinterpret_cast<const T *>(p.v) + b * p.v_bs + (int64_t)h * p.headdim + slice0;
     const char *packs = p.pack + (int64_t)bh * p.nchunks * L::kBytes;
-    // Eight elements per piece; rows past the end repeat the last one (their u
+    // Direct copies: a wave instruction fills 64 consecutive 16-byte pieces of
+    // LDS, each lane from an offset of its own into the chunk's rows.  A row's
+    // padding, columns past N and rows past the end have an offset beyond the
+    // buffer, which reads as 0.  The instructions of a chunk (2 NB + 1 for keys
+    // and for queries, 5 for v, 8 of Tb, Pm and the tables) are dealt to the
+    // four waves; only the buffers' bases move, in scalar registers.
+    constexpr int kRowPieces = 4 * NB + 2, kRowCopies = 2 * NB + 1, kVPieces = Buf::kVRow / 8, kVCopies = C * kVPieces / 64;
+    constexpr int kKeyTurns = (kRowCopies + 3) / 4, kVTurns = (kVCopies + 3) / 4;
+    const int uwave = __builtin_amdgcn_readfirstlane(wave);
+    uint32_t k_off[kKeyTurns], q_off[kKeyTurns], v_off[kVTurns];
+    if constexpr (DIRECT) {
+#pragma unroll
+        for (int i = 0; i < kKeyTurns; ++i) {
+            const int kp = 64 * (4 * i + uwave) + lane, qp = 64 * (4 * i + (3 - uwave)) + lane;
+            const int kn = 8 * (kp % kRowPieces), qn = 8 * (qp % kRowPieces);
+            k_off[i] = kn < N ? 2u * ((uint32_t)(kp / kRowPieces) * (uint32_t)p.k_ts + (uint32_t)kn) : 0xffffff00u;
+            q_off[i] = qn < N ? 2u * ((uint32_t)(qp / kRowPieces) * (uint32_t)p.q_ts + (uint32_t)qn) : 0xffffff00u;
+        }
+#pragma unroll
+        for (int i = 0; i < kVTurns; ++i) {
+            const int vp = 64 * (4 * i + (uwave ^ 1)) + lane, vn = 8 * (vp % kVPieces);
+            v_off[i] = vn < min(kSlice, p.headdim - slice0) ? 2u * ((uint32_t)(vp / kVPieces) * (uint32_t)p.v_ts + (uint32_t)vn)
+                                                            : 0xffffff00u;
+        }
+    }
+    auto copy = [&](__amdgpu_buffer_rsrc_t r, uint32_t off, const void *to) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)to, 16, (int)off, 0, 0, 0);
+    };
+    auto fetch_direct = [&](int64_t c) {
+        const int rows = (int)min(p.seqlen - c * C, (int64_t)C);
+        Buf &to = bufs[c & 1];
+        const __amdgpu_buffer_rsrc_t kr = buffer_rsrc(kbase + c * C * p.k_ts, 2u * (uint32_t)((rows - 1) * p.k_ts + N)),
+                                     qr = buffer_rsrc(qbase + c * C * p.q_ts, 2u * (uint32_t)((rows - 1) * p.q_ts + N)),
+                                     vr = buffer_rsrc(vbase + c * C * p.v_ts,
+                                                      2u * (uint32_t)((rows - 1) * p.v_ts + min(kSlice, p.headdim - slice0))),
+                                     pr = buffer_rsrc(packs + c * L::kBytes, L::kBytes);
+#pragma unroll
+        for (int i = 0; i < kKeyTurns; ++i) {
+            if (4 * i + uwave < kRowCopies) copy(kr, k_off[i], &to.k[0][0][0] + 512 * (4 * i + uwave));
+            if (4 * i + 3 - uwave < kRowCopies) copy(qr, q_off[i], &to.q[0][0][0] + 512 * (4 * i + 3 - uwave));
+        }
+#pragma unroll
+        for (int i = 0; i < kVTurns; ++i)
+            if (4 * i + (uwave ^ 1) < kVCopies) copy(vr, v_off[i], &to.v[0][0] + 512 * (4 * i + (uwave ^ 1)));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) copy(pr, 1024u * (4 * i + uwave) + 16u * lane, to.pack + 1024 * (4 * i + uwave));
+    };
+    // Through registers: eight elements per piece; rows past the end repeat the last one (their u
     // are 0), columns past N are 0.  A thread's pieces keep their rows and
-    // columns, so their addresses only move on by a chunk; the last chunk's may
-    // be cut short, which `cut` sees to.
+    // columns, so their addresses only move on by a chunk; they are taken anew
+    // for the last one, which may be cut short.
     const T *kq_at[NB], *v_at;
     const int v_row = tid >> 3, v_col = 8 * (tid & 7);
     auto piece_of = [&](int i, bool &is_q, int &row, int &n) {
@@ -484,114 +534,122 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         }
     };
 
-    if (N < 32 * NB) {  // columns that no piece fills
+    if (!DIRECT && N < 32 * NB) {  // columns that no piece fills
         for (int i = tid; i < (int)sizeof(bufs) / 16; i += kThreads) reinterpret_cast<u32x4 *>(&bufs[0])[i] = u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
     }
     Regs regs;
-    point(0);
-    fetch(regs, 0);
-    place(regs, bufs[0]);
+    if constexpr (DIRECT) {
+        fetch_direct(0);
+    } else {
+        point(0);
+        fetch(regs, 0);
+        place(regs, bufs[0]);
+    }
+    // Outputs by a buffer over the chunk's rows, which drops those past the end.
+    const uint32_t y_row = (uint32_t)(p.nheads * p.headdim * (int)sizeof(T));
+    const uint32_t y_off = (uint32_t)i16 * y_row + (uint32_t)(((int)h * p.headdim + p0 + 4 * g) * (int)sizeof(T));
     wait_vmcnt<0>();
     __syncthreads();
     const int64_t nc = p.nchunks;
     for (int64_t c = 0; c < nc; ++c) {
         const Buf &buf = bufs[BUFS == 2 ? (int)(c & 1) : 0];
-        if (c + 1 < nc) fetch(regs, c + 1);
+        if (c + 1 < nc) {
+            if constexpr (DIRECT) fetch_direct(c + 1);
+            else fetch(regs, c + 1);
+        }
+        f32x4 qs[2] = {};  // S q, then y
         if (live) {
             const float *tab = reinterpret_cast<const float *>(buf.pack + L::kTab);
-            // S k (rows: tokens) and S q (rows: p).
-            f32x4 ks[2] = {}, qs[2] = {};
+            // The order of what follows is written out, since with two waves per
+            // SIMD at most a read of LDS right before its use costs its latency:
+            // every operand is read one step ahead (a scheduling barrier keeps
+            // it there), and the products that only the outputs need (S q) stand
+            // where the chain S k -> X -> U waits for the matrix cores.
+            auto rows_of = [&](const bf16 (&plane)[NI][C][Buf::kPlane], int kb, bf16x8 (&f)[2][NI]) {
+#pragma unroll
+                for (int I = 0; I < 2; ++I)
+#pragma unroll
+                    for (int e = 0; e < NI; ++e)
+                        f[I][e] = *reinterpret_cast<const bf16x8 *>(&plane[e][16 * I + i16][32 * kb + 8 * g]);
+            };
+            // S k (rows: tokens); the terms of S are kept for S q (rows: p).
+            f32x4 ks[2] = {};
+            bf16x8 sf[NB][NO], kf[2][2][NI], qf[2][2][NI];
+            rows_of(buf.k, 0, kf[0]);
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
+                if (kb + 1 < NB) rows_of(buf.k, kb + 1, kf[(kb + 1) & 1]);
+                else rows_of(buf.q, 0, qf[0]);
+                __builtin_amdgcn_sched_barrier(0);
                 float f[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] = s[kb][i >> 2][i & 3];
-                bf16x8 sf[3];
-                split(f, sf);
+                bf16x8 st[3];
+                split(f, st);
 #pragma unroll
-                for (int I = 0; I < 2; ++I) {
-                    bf16x8 kf[NI], qf[NI];
+                for (int e = 0; e < NO; ++e) sf[kb][e] = st[e];
 #pragma unroll
-                    for (int e = 0; e < NI; ++e) {
-                        kf[e] = *reinterpret_cast<const bf16x8 *>(&buf.k[e][16 * I + i16][32 * kb + 8 * g]);
-                        qf[e] = *reinterpret_cast<const bf16x8 *>(&buf.q[e][16 * I + i16][32 * kb + 8 * g]);
-                    }
-                    mma_terms<NI, 3>(kf, sf, ks[I]);
-                    mma_terms<NO, NI>(sf, qf, qs[I]);
-                }
+                for (int I = 0; I < 2; ++I) mma_terms<NI, 3>(kf[kb & 1][I], st, ks[I]);
             }
-            // X = v - a S k, then U = Tb X.
+            auto s_q = [&](int kb) {
+                if (kb + 1 < NB) rows_of(buf.q, kb + 1, qf[(kb + 1) & 1]);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int I = 0; I < 2; ++I) mma_terms<NO, NI>(sf[kb], qf[kb & 1][I], qs[I]);
+            };
+            // X = v - a S k.
+            f32x4 av[2];
             float x[8];
 #pragma unroll
             for (int I = 0; I < 2; ++I) {
-                const f32x4 a = *reinterpret_cast<const f32x4 *>(tab + L::kA + 16 * I + 4 * g);
-                float v[4];
+                av[I] = *reinterpret_cast<const f32x4 *>(tab + L::kA + 16 * I + 4 * g);
                 if constexpr (sizeof(T) == 2) {
                     const i16x4 t = ds_read_tr16(&buf.v[16 * I + 4 * g + (i16 >> 2)][16 * wave + 4 * (i16 & 3)]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        v[r] = __builtin_bit_cast(float, (uint32_t)(uint16_t)t[r] << 16);
+                    for (int r = 0; r < 4; ++r) x[4 * I + r] = __builtin_bit_cast(float, (uint32_t)(uint16_t)t[r] << 16);
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = buf.v[16 * I + 4 * g + r][16 * wave + i16];
+                    for (int r = 0; r < 4; ++r) x[4 * I + r] = buf.v[16 * I + 4 * g + r][16 * wave + i16];
                 }
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[4 * I + r] = fmaf(-a[r], ks[I][r], v[r]);
             }
-            bf16x8 xf[3];
+            s_q(0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = fmaf(-av[i >> 2][i & 3], ks[i >> 2][i & 3], x[i]);
+            // U = Tb X.
+            bf16x4 t0[3], x0[3];
+            bf16x8 t1[3], xf[3];
+#pragma unroll
+            for (int e = 0; e < 3; ++e) {
+                t0[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + L::kT0 + (e * 64 + lane) * 8);
+                t1[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + L::kT1 + (e * 64 + lane) * 16);
+            }
+            if (NB > 1) s_q(1);
+            else __builtin_amdgcn_sched_barrier(0);
             split(x, xf);
-            f32x4 u[2] = {};
-            {
-                bf16x4 t0[3], x0[3];
-                bf16x8 t1[3];
 #pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    t0[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + L::kT0 + (e * 64 + lane) * 8);
-                    t1[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + L::kT1 + (e * 64 + lane) * 16);
-                    x0[e] = bf16x4{xf[e][0], xf[e][1], xf[e][2], xf[e][3]};
-                }
-                mma_terms<3, 3>(t0, x0, u[0]);
-                mma_terms<3, 3>(t1, xf, u[1]);
+            for (int e = 0; e < 3; ++e) x0[e] = bf16x4{xf[e][0], xf[e][1], xf[e][2], xf[e][3]};
+            f32x4 u[2] = {}, dv[2];
+            mma_terms<3, 3>(t0, x0, u[0]);
+            mma_terms<3, 3>(t1, xf, u[1]);
+#pragma unroll
+            for (int kb = 2; kb < NB; ++kb) s_q(kb);
+            bf16x8 p1[NO];
+            bf16x4 pm0[NO];
+            float cv[2];
+#pragma unroll
+            for (int e = 0; e < NO; ++e) {
+                pm0[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + L::kP0 + (e * 64 + lane) * 8);
+                p1[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + L::kP1 + (e * 64 + lane) * 16);
             }
-            // y: rows p = p0 + 4 g + r, column: token 16 I + i16.
-            {
-                float uv[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3];
-                bf16x8 uf[NO], p1[NO];
-                bf16x4 u0[NO], pm0[NO];
-                split(uv, uf);
-#pragma unroll
-                for (int e = 0; e < NO; ++e) {
-                    u0[e] = bf16x4{uf[e][0], uf[e][1], uf[e][2], uf[e][3]};
-                    pm0[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + L::kP0 + (e * 64 + lane) * 8);
-                    p1[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + L::kP1 + (e * 64 + lane) * 16);
-                }
-#pragma unroll
-                for (int I = 0; I < 2; ++I) {
-                    const float ci = tab[L::kC + 16 * I + i16];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) qs[I][r] *= ci;
-                }
-                mma_terms<NO, NO>(u0, pm0, qs[0]);
-                mma_terms<NO, NO>(uf, p1, qs[1]);
-#pragma unroll
-                for (int I = 0; I < 2; ++I) {
-                    const int64_t t = c * C + 16 * I + i16;
-                    T *to = reinterpret_cast<T *>(p.y) + (((int64_t)b * p.seqlen + t) * p.nheads + h) * p.headdim + p0 + 4 * g;
-                    if (t < p.seqlen) {
-                        if constexpr (sizeof(T) == 2) {
-                            const bf16x4 o = {(bf16)qs[I][0], (bf16)qs[I][1], (bf16)qs[I][2], (bf16)qs[I][3]};
-                            *reinterpret_cast<u32x2_at2 *>(to) = __builtin_bit_cast(u32x2, o);
-                        } else {
-                            store_words(to, __builtin_bit_cast(u32x4, qs[I]));
-                        }
-                    }
-                }
+            for (int I = 0; I < 2; ++I) {
+                cv[I] = tab[L::kC + 16 * I + i16];
+                dv[I] = *reinterpret_cast<const f32x4 *>(tab + L::kD + 16 * I + 4 * g);
             }
-            // The state after the accepted index, then after the chunk.
-            if (at >= c * C && at < c * C + C) {
+            const float end = tab[L::kEnd];
+            __builtin_amdgcn_sched_barrier(0);
+            if (at >= c * C && at < c * C + C) {  // the state after the accepted index
                 const float *wt = p.at_tables + (int64_t)bh * kAtFloats;
                 const float e = wt[C];
                 float uv[8];
@@ -604,40 +662,92 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        bf16x8 kf[NI];
-                        keys_t(buf, kb, half, kf);
+                        bf16x8 kt[NI];
+                        keys_t(buf, kb, half, kt);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) m[kb][half][r] = s[kb][half][r] * e;
-                        mma_terms<NI, 3>(kf, uf, m[kb][half]);
+                        mma_terms<NI, 3>(kt, uf, m[kb][half]);
                     }
                 store_state(m, p.state_out);
             }
+            // The state after the chunk.
             {
-                const float e = tab[L::kEnd];
+                bf16x8 kt[2][NI];
+                keys_t(buf, 0, 0, kt[0]);
+                keys_t(buf, 0, 1, kt[1]);
+                __builtin_amdgcn_sched_barrier(0);
                 float uv[8];
 #pragma unroll
-                for (int I = 0; I < 2; ++I) {
-                    const f32x4 d = *reinterpret_cast<const f32x4 *>(tab + L::kD + 16 * I + 4 * g);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) uv[4 * I + r] = u[I][r] * d[r];
-                }
+                for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3] * dv[i >> 2][i & 3];
                 bf16x8 uf[3];
                 split(uv, uf);
 #pragma unroll
-                for (int kb = 0; kb < NB; ++kb)
+                for (int kb = 0; kb < NB; ++kb) {
+                    bf16x8 next[2][NI];
+                    if (kb + 1 < NB) {
+                        keys_t(buf, kb + 1, 0, next[0]);
+                        keys_t(buf, kb + 1, 1, next[1]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        bf16x8 kf[NI];
-                        keys_t(buf, kb, half, kf);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) s[kb][half][r] *= e;
-                        mma_terms<NI, 3>(kf, uf, s[kb][half]);
+                        for (int r = 0; r < 4; ++r) s[kb][half][r] *= end;
+                        mma_terms<NI, 3>(kt[half], uf, s[kb][half]);
                     }
+                    if (kb + 1 < NB)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+#pragma unroll
+                            for (int e = 0; e < NI; ++e) kt[half][e] = next[half][e];
+                }
+            }
+            // y: rows p = p0 + 4 g + r, column: token 16 I + i16.
+            {
+                float uv[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3];
+                bf16x8 uf[NO];
+                bf16x4 u0[NO];
+                split(uv, uf);
+#pragma unroll
+                for (int e = 0; e < NO; ++e) u0[e] = bf16x4{uf[e][0], uf[e][1], uf[e][2], uf[e][3]};
+#pragma unroll
+                for (int I = 0; I < 2; ++I)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) qs[I][r] *= cv[I];
+                mma_terms<NO, NO>(u0, pm0, qs[0]);
+                mma_terms<NO, NO>(uf, p1, qs[1]);
             }
         }
-        if (BUFS == 2) wait_vmcnt<0>();  // the copies into the other buffer
+        // The loads of the next chunk are waited for before the outputs are
+        // stored: the counter would make the wait include the stores.
+        if (BUFS == 2) wait_vmcnt<0>();  // among them the copies into the other buffer
         else __syncthreads();            // the only buffer is read no more
-        if (c + 1 < nc) place(regs, bufs[BUFS == 2 ? (int)((c + 1) & 1) : 0]);
+        if (!DIRECT && c + 1 < nc) place(regs, bufs[BUFS == 2 ? (int)((c + 1) & 1) : 0]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (live)
+#pragma unroll
+            for (int I = 0; I < 2; ++I) {
+                if constexpr (DIRECT) {
+                    const uint32_t rows = (uint32_t)min(p.seqlen - c * C, (int64_t)C);
+                    const __amdgpu_buffer_rsrc_t yr = buffer_rsrc(
+                        reinterpret_cast<char *>(p.y) + ((int64_t)b * p.seqlen + c * C) * (int64_t)y_row, rows * y_row);
+                    const bf16x4 o = {(bf16)qs[I][0], (bf16)qs[I][1], (bf16)qs[I][2], (bf16)qs[I][3]};
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), yr, (int)(y_off + 16u * I * y_row), 0, 0);
+                } else {
+                    const int64_t t = c * C + 16 * I + i16;
+                    T *to = reinterpret_cast<T *>(p.y) + (((int64_t)b * p.seqlen + t) * p.nheads + h) * p.headdim + p0 + 4 * g;
+                    if (t < p.seqlen) {
+                        if constexpr (sizeof(T) == 2) {
+                            const bf16x4 o = {(bf16)qs[I][0], (bf16)qs[I][1], (bf16)qs[I][2], (bf16)qs[I][3]};
+                            *reinterpret_cast<u32x2_at2 *>(to) = __builtin_bit_cast(u32x2, o);
+                        } else {
+                            store_words(to, __builtin_bit_cast(u32x4, qs[I]));
+                        }
+                    }
+                }
+            }
         __syncthreads();
     }
     if (p.final_state) store_state(s, p.final_state);
@@ -650,7 +760,20 @@ hipError_t launch_chunks(const DeltaParams &p, hipStream_t stream) {
     static_assert(BUFS * sizeof(Buffer<T, NB>) <= kLds, "LDS");
     const int64_t items = p.batch * p.nheads * ((p.headdim + kSlice - 1) / kSlice);
     constexpr int WAVES = 2 * BUFS * sizeof(Buffer<T, NB>) <= kLds && NB <= 5 ? 2 : 1;
-    delta_chunks<T, NB, BUFS, WAVES><<<(unsigned)items, kThreads, 0, stream>>>(p);
+    if constexpr (sizeof(T) == 2) {
+        // Direct copies need rows of 16-byte alignment and 32-bit offsets within a
+        // chunk (the last byte below 2^31, so that the mark of no element is out).
+        auto fits = [&](const void *base, int64_t bs, int64_t ts, int64_t inner) {
+            return (uintptr_t)base % 16 == 0 && bs % 8 == 0 && ts % 8 == 0 && C * ts + inner < ((int64_t)1 << 30);
+        };
+        const int64_t y_bytes = (int64_t)C * p.nheads * p.headdim * 2;
+        if (fits(p.q, p.q_bs, p.q_ts, 256) && fits(p.k, p.k_bs, p.k_ts, 256) && fits(p.v, p.v_bs, p.v_ts, 256) &&
+            (uintptr_t)p.y % 16 == 0 && y_bytes < ((int64_t)1 << 31)) {
+            delta_chunks<T, NB, BUFS, WAVES, true><<<(unsigned)items, kThreads, 0, stream>>>(p);
+            return hipGetLastError();
+        }
+    }
+    delta_chunks<T, NB, BUFS, WAVES, false><<<(unsigned)items, kThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
