@@ -320,10 +320,26 @@ __global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
 }
 
 // ------------------------------------------------------------------- chunks
+// LDS of a chunk.  Rows of keys and queries (4 NB pieces of 16 bytes) are not
+// padded, so that a copy may fill them in order; instead the pieces of row r
+// stand at piece ^ key_swz(r).  Both ways of reading then meet every bank once:
+// the same piece of 16 rows, and (transposed) four pieces of four rows.
+template <int NB>
+__device__ __forceinline__ int key_swz(int r) {
+    int s = (r >> 2) & 3;                            // rows that are a multiple of 256 bytes apart
+    if constexpr (NB % 4 == 0) s |= 4 * (r & 3);
+    else if constexpr (NB % 2 == 0) s |= 4 * ((r >> 1) & 1);
+    return s;
+}
+// v: rows of 64 values; bf16 ones are read transposed, two pieces of four rows.
+template <typename T>
+__device__ __forceinline__ int v_swz(int r) {
+    return sizeof(T) == 2 ? 2 * ((r >> 1) & 3) : 0;
+}
 template <typename T, int NB>
 struct Buffer {
-    static constexpr int kPlane = 32 * NB + 16;  // elements of a row of keys or queries, padded by 32 bytes
-    static constexpr int kVRow = kSlice + 32 / (int)sizeof(T);
+    static constexpr int kPlane = 32 * NB;           // elements of a row of keys or queries
+    static constexpr int kVRow = kSlice + (sizeof(T) == 2 ? 0 : 8);
     alignas(16) bf16 k[kIn<T>][C][kPlane];
     alignas(16) bf16 q[kIn<T>][C][kPlane];
     alignas(16) T v[C][kVRow];
@@ -349,7 +365,11 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     typedef Carry<T, NB> Regs;
     constexpr int NI = kIn<T>, NO = kOut<T>;
     static_assert(!DIRECT || (sizeof(T) == 2 && BUFS == 2 && L::kBytes == 8 * 1024), "direct copies");
-    __shared__ Buf bufs[BUFS];
+    // Two objects, so that the compiler knows reads of one apart from the copies
+    // into the other and does not make them wait.
+    __shared__ Buf buf0;
+    __shared__ std::conditional_t<BUFS == 2, Buf, char> buf1_;
+    Buf &buf1 = *reinterpret_cast<Buf *>(BUFS == 2 ? (void *)&buf1_ : (void *)&buf0);
 
     // Consecutive items (the slices of a head, the heads of a group) on one XCD.
     const unsigned xcd = blockIdx.x % 8, whole = gridDim.x / 8, more = gridDim.x % 8;
@@ -367,51 +387,47 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     const T *vbase = reinterpret_cast<const T *>(p.v) + b * p.v_bs + (int64_t)h * p.headdim + slice0;
     const char *packs = p.pack + (int64_t)bh * p.nchunks * L::kBytes;
     // Direct copies: a wave instruction fills 64 consecutive 16-byte pieces of
-    // LDS, each lane from an offset of its own into the chunk's rows.  A row's
-    // padding, columns past N and rows past the end have an offset beyond the
-    // buffer, which reads as 0.  The instructions of a chunk (2 NB + 1 for keys
-    // and for queries, 5 for v, 8 of Tb, Pm and the tables) are dealt to the
-    // four waves; only the buffers' bases move, in scalar registers.
-    constexpr int kRowPieces = 4 * NB + 2, kRowCopies = 2 * NB + 1, kVPieces = Buf::kVRow / 8, kVCopies = C * kVPieces / 64;
-    constexpr int kKeyTurns = (kRowCopies + 3) / 4, kVTurns = (kVCopies + 3) / 4;
+    // LDS, each lane from an offset of its own into the chunk's rows.  Columns
+    // past N and rows past the end lie beyond the buffer, which reads as 0.  A
+    // wave issues NB of the keys' and queries' 4 NB instructions, one of v's
+    // four and two of the eight of Tb, Pm and the tables; only the buffers'
+    // bases move, in scalar registers.  They are spread over the steps of the
+    // chunk before (fetch_step): the texture path takes 64 bytes a cycle, and a
+    // wave that issues all of its copies at once waits for it (670 of 4700
+    // cycles of a chunk).  Nothing branches: the last chunk's copies of a chunk
+    // that is not there read an empty buffer.
     const int uwave = __builtin_amdgcn_readfirstlane(wave);
-    uint32_t k_off[kKeyTurns], q_off[kKeyTurns], v_off[kVTurns];
+    constexpr int kSteps = NB + 3;
+    uint32_t kq_off[NB], v_off;
+    auto is_query = [&](int k) { return 4 * k + uwave >= 2 * NB; };
     if constexpr (DIRECT) {
 #pragma unroll
-        for (int i = 0; i < kKeyTurns; ++i) {
-            const int kp = 64 * (4 * i + uwave) + lane, qp = 64 * (4 * i + (3 - uwave)) + lane;
-            const int kn = 8 * (kp % kRowPieces), qn = 8 * (qp % kRowPieces);
-            k_off[i] = kn < N ? 2u * ((uint32_t)(kp / kRowPieces) * (uint32_t)p.k_ts + (uint32_t)kn) : 0xffffff00u;
-            q_off[i] = qn < N ? 2u * ((uint32_t)(qp / kRowPieces) * (uint32_t)p.q_ts + (uint32_t)qn) : 0xffffff00u;
+        for (int k = 0; k < NB; ++k) {
+            const int at = 64 * (4 * k + uwave - (is_query(k) ? 2 * NB : 0)) + lane, row = at / (4 * NB);
+            const int n = 8 * ((at % (4 * NB)) ^ key_swz<NB>(row));
+            kq_off[k] = n < N ? 2u * ((uint32_t)row * (uint32_t)(is_query(k) ? p.q_ts : p.k_ts) + (uint32_t)n) : 0xffffff00u;
         }
-#pragma unroll
-        for (int i = 0; i < kVTurns; ++i) {
-            const int vp = 64 * (4 * i + (uwave ^ 1)) + lane, vn = 8 * (vp % kVPieces);
-            v_off[i] = vn < min(kSlice, p.headdim - slice0) ? 2u * ((uint32_t)(vp / kVPieces) * (uint32_t)p.v_ts + (uint32_t)vn)
-                                                            : 0xffffff00u;
-        }
+        const int at = 64 * uwave + lane, row = at / 8, n = 8 * ((at % 8) ^ v_swz<T>(row));
+        v_off = n < min(kSlice, p.headdim - slice0) ? 2u * ((uint32_t)row * (uint32_t)p.v_ts + (uint32_t)n) : 0xffffff00u;
     }
-    auto copy = [&](__amdgpu_buffer_rsrc_t r, uint32_t off, const void *to) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)to, 16, (int)off, 0, 0, 0);
+    auto copy = [&](const void *base, int rows, int64_t ts, int inner, uint32_t off, void *to) {
+        const uint32_t bytes = rows > 0 ? 2u * (uint32_t)((rows - 1) * (int)ts + inner) : 0u;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(base, bytes), (__attribute__((address_space(3))) void *)to, 16,
+                                                 (int)off, 0, 0, 0);
     };
-    auto fetch_direct = [&](int64_t c) {
-        const int rows = (int)min(p.seqlen - c * C, (int64_t)C);
-        Buf &to = bufs[c & 1];
-        const __amdgpu_buffer_rsrc_t kr = buffer_rsrc(kbase + c * C * p.k_ts, 2u * (uint32_t)((rows - 1) * p.k_ts + N)),
-                                     qr = buffer_rsrc(qbase + c * C * p.q_ts, 2u * (uint32_t)((rows - 1) * p.q_ts + N)),
-                                     vr = buffer_rsrc(vbase + c * C * p.v_ts,
-                                                      2u * (uint32_t)((rows - 1) * p.v_ts + min(kSlice, p.headdim - slice0))),
-                                     pr = buffer_rsrc(packs + c * L::kBytes, L::kBytes);
-#pragma unroll
-        for (int i = 0; i < kKeyTurns; ++i) {
-            if (4 * i + uwave < kRowCopies) copy(kr, k_off[i], &to.k[0][0][0] + 512 * (4 * i + uwave));
-            if (4 * i + 3 - uwave < kRowCopies) copy(qr, q_off[i], &to.q[0][0][0] + 512 * (4 * i + 3 - uwave));
+    auto fetch_step = [&](int64_t c, int k, Buf &to) __attribute__((always_inline)) {
+        const int rows = (int)max(min(p.seqlen - c * C, (int64_t)C), (int64_t)0);
+        if (k < NB) {
+            const bool q = is_query(k);
+            const int64_t ts = q ? p.q_ts : p.k_ts;
+            copy((q ? qbase : kbase) + c * C * ts, rows, ts, N, kq_off[k],
+                 q ? &to.q[0][0][0] + 512 * (4 * k + uwave - 2 * NB) : &to.k[0][0][0] + 512 * (4 * k + uwave));
+        } else if (k == NB) {
+            copy(vbase + c * C * p.v_ts, rows, p.v_ts, min(kSlice, p.headdim - slice0), v_off, &to.v[0][0] + 512 * uwave);
+        } else {
+            const int at = 1024 * (4 * (k - NB - 1) + uwave);
+            copy(packs + c * L::kBytes, min(rows, 1), 0, L::kBytes / 2, (uint32_t)at + 16u * lane, to.pack + at);
         }
-#pragma unroll
-        for (int i = 0; i < kVTurns; ++i)
-            if (4 * i + (uwave ^ 1) < kVCopies) copy(vr, v_off[i], &to.v[0][0] + 512 * (4 * i + (uwave ^ 1)));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) copy(pr, 1024u * (4 * i + uwave) + 16u * lane, to.pack + 1024 * (4 * i + uwave));
     };
     // Through registers: eight elements per piece; rows past the end repeat the last one (their u
     // are 0), columns past N are 0.  A thread's pieces keep their rows and
@@ -438,7 +454,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         }
         v_at = vbase + (c * C + min(v_row, left)) * p.v_ts + min(v_col, p.headdim - slice0 - 8);
     };
-    auto fetch = [&](Regs &r, int64_t c) {
+    auto fetch = [&](Regs &r, int64_t c, Buf &to) __attribute__((always_inline)) {
         if (c + 1 == p.nchunks && c > 0) point(c);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -455,11 +471,10 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         const char *src = packs + c * L::kBytes;
         if constexpr (BUFS == 2) {
             // The other buffer's last reader is behind the last barrier.
-            char *to = bufs[c & 1].pack;
 #pragma unroll
             for (int i = 0; i < Regs::kPackWords; ++i) {
                 const int at = 16 * (kThreads * i + 64 * wave);
-                if (at + 1024 <= L::kBytes || at + 16 * lane < L::kBytes) copy16_to_lds(src + at + 16 * lane, to + at);
+                if (at + 1024 <= L::kBytes || at + 16 * lane < L::kBytes) copy16_to_lds(src + at + 16 * lane, to.pack + at);
             }
         } else {
 #pragma unroll
@@ -474,8 +489,9 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             int row, n;
             piece_of(i, is_q, row, n);
             if (n >= N) continue;
+            const int sw = 8 * key_swz<NB>(row);
             if constexpr (NI == 1) {
-                *reinterpret_cast<u32x4 *>(is_q ? &to.q[0][row][n] : &to.k[0][row][n]) = r.kq[i][0];
+                *reinterpret_cast<u32x4 *>(is_q ? &to.q[0][row][n ^ sw] : &to.k[0][row][n ^ sw]) = r.kq[i][0];
             } else {
                 float f[8];
 #pragma unroll
@@ -483,12 +499,13 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 bf16x8 t[3];
                 split(f, t);
 #pragma unroll
-                for (int e = 0; e < NI; ++e) *reinterpret_cast<bf16x8 *>(is_q ? &to.q[e][row][n] : &to.k[e][row][n]) = t[e];
+                for (int e = 0; e < NI; ++e)
+                    *reinterpret_cast<bf16x8 *>(is_q ? &to.q[e][row][n ^ sw] : &to.k[e][row][n ^ sw]) = t[e];
             }
         }
 #pragma unroll
         for (int j = 0; j < Regs::WORDS; ++j)
-            *reinterpret_cast<u32x4 *>(&to.v[tid >> 3][8 * (tid & 7) + j * Regs::VEC]) = r.v[j];
+            *reinterpret_cast<u32x4 *>(&to.v[v_row][(v_col ^ 8 * v_swz<T>(v_row)) + j * Regs::VEC]) = r.v[j];
         if constexpr (BUFS == 1)
 #pragma unroll
             for (int i = 0; i < Regs::kPackWords; ++i)
@@ -527,7 +544,9 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     auto keys_t = [&](const Buf &buf, int kb, int half, bf16x8 (&f)[NI]) {
 #pragma unroll
         for (int e = 0; e < NI; ++e) {
-            const bf16 *src = &buf.k[e][4 * g + (i16 >> 2)][32 * kb + 8 * (i16 & 3) + 4 * half];
+            // Row r + 16 has the swizzle of row r.
+            const int row = 4 * g + (i16 >> 2);
+            const bf16 *src = &buf.k[e][row][((32 * kb + 8 * (i16 & 3)) ^ 8 * key_swz<NB>(row)) + 4 * half];
             const i16x4 lo = ds_read_tr16(src), hi = ds_read_tr16(src + 16 * Buf::kPlane);
             typedef short i16x8 __attribute__((ext_vector_type(8)));
             f[e] = __builtin_bit_cast(bf16x8, (i16x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
@@ -535,16 +554,18 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     };
 
     if (!DIRECT && N < 32 * NB) {  // columns that no piece fills
-        for (int i = tid; i < (int)sizeof(bufs) / 16; i += kThreads) reinterpret_cast<u32x4 *>(&bufs[0])[i] = u32x4{0u, 0u, 0u, 0u};
+        for (int i = tid; i < (int)sizeof(Buf) / 16; i += kThreads)
+            reinterpret_cast<u32x4 *>(&buf0)[i] = reinterpret_cast<u32x4 *>(&buf1)[i] = u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
     }
     Regs regs;
     if constexpr (DIRECT) {
-        fetch_direct(0);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) fetch_step(0, k, buf0);
     } else {
         point(0);
-        fetch(regs, 0);
-        place(regs, bufs[0]);
+        fetch(regs, 0, buf0);
+        place(regs, buf0);
     }
     // Outputs by a buffer over the chunk's rows, which drops those past the end.
     const uint32_t y_row = (uint32_t)(p.nheads * p.headdim * (int)sizeof(T));
@@ -552,12 +573,17 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     wait_vmcnt<0>();
     __syncthreads();
     const int64_t nc = p.nchunks;
-    for (int64_t c = 0; c < nc; ++c) {
-        const Buf &buf = bufs[BUFS == 2 ? (int)(c & 1) : 0];
-        if (c + 1 < nc) {
-            if constexpr (DIRECT) fetch_direct(c + 1);
-            else fetch(regs, c + 1);
-        }
+    // One chunk from `buf`, while the next one comes into `other`.
+    auto chunk = [&](int64_t c, const Buf &buf, Buf &other) __attribute__((always_inline)) {
+        if (!DIRECT && c + 1 < nc) fetch(regs, c + 1, other);
+        // A wave without rows issues its copies at once.
+        auto fetch_some = [&](int from, int to) {
+            if constexpr (DIRECT)
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+                    if (k >= from && k < to) fetch_step(c + 1, k, other);
+        };
+        if (!live) fetch_some(0, kSteps);
         f32x4 qs[2] = {};  // S q, then y
         if (live) {
             const float *tab = reinterpret_cast<const float *>(buf.pack + L::kTab);
@@ -571,7 +597,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 for (int I = 0; I < 2; ++I)
 #pragma unroll
                     for (int e = 0; e < NI; ++e)
-                        f[I][e] = *reinterpret_cast<const bf16x8 *>(&plane[e][16 * I + i16][32 * kb + 8 * g]);
+                        f[I][e] = *reinterpret_cast<const bf16x8 *>(
+                            &plane[e][16 * I + i16][(32 * kb + 8 * g) ^ 8 * key_swz<NB>(i16)]);
             };
             // S k (rows: tokens); the terms of S are kept for S q (rows: p).
             f32x4 ks[2] = {};
@@ -581,6 +608,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             for (int kb = 0; kb < NB; ++kb) {
                 if (kb + 1 < NB) rows_of(buf.k, kb + 1, kf[(kb + 1) & 1]);
                 else rows_of(buf.q, 0, qf[0]);
+                fetch_some(kb, kb + 1);
                 __builtin_amdgcn_sched_barrier(0);
                 float f[8];
 #pragma unroll
@@ -594,6 +622,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             }
             auto s_q = [&](int kb) {
                 if (kb + 1 < NB) rows_of(buf.q, kb + 1, qf[(kb + 1) & 1]);
+                fetch_some(NB + (kb == 0 ? 0 : kb + 1), kb + 1 == NB ? kSteps : NB + kb + 2);
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int I = 0; I < 2; ++I) mma_terms<NO, NI>(sf[kb], qf[kb & 1][I], qs[I]);
@@ -605,7 +634,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             for (int I = 0; I < 2; ++I) {
                 av[I] = *reinterpret_cast<const f32x4 *>(tab + L::kA + 16 * I + 4 * g);
                 if constexpr (sizeof(T) == 2) {
-                    const i16x4 t = ds_read_tr16(&buf.v[16 * I + 4 * g + (i16 >> 2)][16 * wave + 4 * (i16 & 3)]);
+                    const int row = 16 * I + 4 * g + (i16 >> 2), col = 16 * wave + 4 * (i16 & 3);
+                    const i16x4 t = ds_read_tr16(&buf.v[row][col ^ 8 * v_swz<T>(row)]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) x[4 * I + r] = __builtin_bit_cast(float, (uint32_t)(uint16_t)t[r] << 16);
                 } else {
@@ -724,7 +754,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         // stored: the counter would make the wait include the stores.
         if (BUFS == 2) wait_vmcnt<0>();  // among them the copies into the other buffer
         else __syncthreads();            // the only buffer is read no more
-        if (!DIRECT && c + 1 < nc) place(regs, bufs[BUFS == 2 ? (int)((c + 1) & 1) : 0]);
+        if (!DIRECT && c + 1 < nc) place(regs, other);
         __builtin_amdgcn_sched_barrier(0);
         if (live)
 #pragma unroll
@@ -749,6 +779,14 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 }
             }
         __syncthreads();
+    };
+    if constexpr (BUFS == 2) {
+        for (int64_t c = 0; c < nc; c += 2) {
+            chunk(c, buf0, buf1);
+            if (c + 1 < nc) chunk(c + 1, buf1, buf0);
+        }
+    } else {
+        for (int64_t c = 0; c < nc; ++c) chunk(c, buf0, buf0);
     }
     if (p.final_state) store_state(s, p.final_state);
 }
