@@ -56,15 +56,20 @@ struct Pack32 {
 };
 constexpr int kAtFloats = 36;  // the accepted index's weights [32] and decay, per (sequence, head)
 
-// 2^d for d in fp64: the whole part goes into the exponent, so the result is
-// off by the hardware exponential's unit however large d is.
-__device__ __forceinline__ float exp2_f64(double d) {
-    d = fmin(fmax(d, -1000.0), 1000.0);
-    const double n = rint(d);
-    return ldexpf(exp2_hw((float)(d - n)), (int)n);
+// A sum of log decays in two floats, its rounding and what that left: sums of a
+// chunk may be large where their differences are small.
+struct TwoFloats {
+    float hi, lo;
+};
+__device__ __forceinline__ TwoFloats two_floats(double v) {
+    const float hi = (float)v;
+    return {hi, (float)(v - (double)hi)};
 }
-
-__device__ __forceinline__ float bf16_f32(bf16 v) { return (float)v; }
+// 2^(a - b): off by |a - b| 2^-24 of itself beside the hardware exponential's
+// unit, which is below 2^-24 absolutely where a <= b.
+__device__ __forceinline__ float exp2_diff(const TwoFloats &a, const TwoFloats &b) {
+    return exp2_hw((a.hi - b.hi) + (a.lo - b.lo));
+}
 
 // v as a sum of N bf16 terms, each the next 8 bits of the fraction (cut off, so
 // that three terms are v itself and two leave less than 2^-15 of it).  A pair of
@@ -112,21 +117,21 @@ __device__ __forceinline__ void mma_terms(const V (&a)[NA], const V (&b)[NB], f3
 }
 
 // ------------------------------------------------------------------ prepare
-template <typename T> __device__ __forceinline__ void load_frag(Frag<T> &f, const T *p, bool valid);
-template <> __device__ __forceinline__ void load_frag<bf16>(Frag<bf16> &f, const bf16 *p, bool valid) {
-    f.zero();
-    if (valid) f.v = __builtin_bit_cast(bf16x8, load_words(p));
+template <typename T> __device__ __forceinline__ void load_frag(Frag<T> &f, const T *p);
+template <> __device__ __forceinline__ void load_frag<bf16>(Frag<bf16> &f, const bf16 *p) {
+    f.v = __builtin_bit_cast(bf16x8, load_words(p));
 }
-template <> __device__ __forceinline__ void load_frag<float>(Frag<float> &f, const float *p, bool valid) {
-    f.zero();
-    if (valid) {
-        f.lo = __builtin_bit_cast(f32x4, load_words(p));
-        f.hi = __builtin_bit_cast(f32x4, load_words(p + 4));
-    }
+template <> __device__ __forceinline__ void load_frag<float>(Frag<float> &f, const float *p) {
+    f.lo = __builtin_bit_cast(f32x4, load_words(p));
+    f.hi = __builtin_bit_cast(f32x4, load_words(p + 4));
 }
 __device__ __forceinline__ float squares(const Frag<bf16> &f, float s) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(bf16_f32(f.v[i]), bf16_f32(f.v[i]), s);
+    for (int i = 0; i < 8; i += 2) {
+        const bf16x2 v = {f.v[i], f.v[i + 1]};
+        s = __builtin_amdgcn_fdot2_f32_bf16(v, v, s, false);
+    }
     return s;
 }
 __device__ __forceinline__ float squares(const Frag<float> &f, float s) {
@@ -141,33 +146,59 @@ __device__ __forceinline__ f32x4 mma_f32_16(const f32x4 &a, const f32x4 &b, f32x
 }
 
 struct WaveTables {
-    double cs2[C];       // Gam_i log2 e
+    float hi[C], lo[C];  // Gam_i log2 e
     float beta[C], kr[C], qr[C];
     float at[2][16][20];  // A's diagonal blocks, transposed: [j][m]; rows padded
     float tb[2][16][20];  // their inverses, row-major
 };
+
+// Orders a wave's own accesses to LDS (which the hardware takes in order).
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
 
 // A wave per (b, chunk, head).  Every 16 x 16 tile is computed transposed, so
 // that lane l holds row i = l%16 and columns j = 4 (l/16) + r: the layout in which
 // delta_chunks feeds it to the matrix cores.  The inverse takes the two diagonal
 // blocks by substitution (a lane per row: t_j = [j = i] - sum_{m>j} t_m A_mj) and
 // joins them, -T11 A10 T00, by fp32 products.
-template <typename T>
+template <typename T, int NB>
 __global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
     __shared__ WaveTables tables[kThreads / 64];
-    WaveTables &w = tables[threadIdx.x >> 6];
+    const int uwave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    WaveTables &w = tables[uwave];
     const int lane = threadIdx.x & 63, i16 = lane & 15, g = lane >> 4;
-    const int64_t items = p.batch * p.nchunks * p.nheads;
-    const int64_t mine = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6), item = min(mine, items - 1);
-    const int h = (int)(item % p.nheads);
-    const int64_t bc = item / p.nheads, b = bc / p.nchunks, c = bc - b * p.nchunks, t0 = c * C;
-    const int group = h / p.heads_per_group;
+    const unsigned items = (unsigned)(p.batch * p.nchunks * p.nheads), item = blockIdx.x * (kThreads / 64) + uwave;
+    if (item >= items) return;
+    const unsigned bc = item / (unsigned)p.nheads, h = item - bc * (unsigned)p.nheads;
+    const unsigned b = bc / (unsigned)p.nchunks, c = bc - b * (unsigned)p.nchunks;
+    const int64_t t0 = (int64_t)c * C;
+    const int left = (int)min(p.seqlen - t0, (int64_t)C);  // tokens of this chunk
+    const int group = (int)h / p.heads_per_group;
+
+    // Keys and queries: rows of token tile I in lanes i16.
+    const T *kbase = reinterpret_cast<const T *>(p.k) + b * p.k_bs + t0 * p.k_ts + (int64_t)group * p.dstate;
+    const T *qbase = reinterpret_cast<const T *>(p.q) + b * p.q_bs + t0 * p.q_ts + (int64_t)group * p.dstate;
+    Frag<T> kf[NB][2], qf[NB][2];
+#pragma unroll
+    for (int I = 0; I < 2; ++I) {
+        const int t = min(16 * I + i16, left - 1);
+        const T *kr = kbase + t * p.k_ts + 8 * g, *qr = qbase + t * p.q_ts + 8 * g;
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) {
+            const bool in = 32 * kb + 8 * g < p.dstate;  // else the row's first piece, made zero below
+            load_frag<T>(kf[kb][I], kr + (in ? 32 * kb : -8 * g));
+            load_frag<T>(qf[kb][I], qr + (in ? 32 * kb : -8 * g));
+        }
+    }
 
     // Tables of the tokens, a lane each; past the end nothing is written
     // (beta 0) and nothing decays.
     double gam = 0.0;
     float beta = 0.0f;
-    if (lane < C && t0 + lane < p.seqlen) {
+    if (lane < left) {
         if (p.g) gam = (double)p.g[b * p.g_bs + (t0 + lane) * p.g_ts + h] * 1.4426950408889634;
         beta = p.beta[b * p.beta_bs + (t0 + lane) * p.beta_ts + h];
     }
@@ -176,91 +207,95 @@ __global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
         const double o = __shfl_up(gam, m);
         if (lane >= m) gam += o;
     }
+    const TwoFloats mine = two_floats(gam);
     if (lane < C) {
-        w.cs2[lane] = gam;
+        w.hi[lane] = mine.hi;
+        w.lo[lane] = mine.lo;
         w.beta[lane] = beta;
     }
 
     // Products of keys with keys and queries: tile (I, J) = lanes (i in I, j in J).
-    const T *kbase = reinterpret_cast<const T *>(p.k) + b * p.k_bs + (int64_t)group * p.dstate;
-    const T *qbase = reinterpret_cast<const T *>(p.q) + b * p.q_bs + (int64_t)group * p.dstate;
-    const T *krow[2], *qrow[2];
-#pragma unroll
-    for (int I = 0; I < 2; ++I) {
-        const int64_t t = min(t0 + 16 * I + i16, p.seqlen - 1);
-        krow[I] = kbase + t * p.k_ts;
-        qrow[I] = qbase + t * p.q_ts;
-    }
     f32x4 kk[3] = {}, qk[3] = {};  // tiles 00, 10, 11
     float ksq[2] = {0.f, 0.f}, qsq[2] = {0.f, 0.f};
-    for (int n = 8 * g; n - 8 * g < p.dstate; n += 32) {
-        Frag<T> k[2], q[2];
 #pragma unroll
-        for (int I = 0; I < 2; ++I) {
-            load_frag<T>(k[I], krow[I] + n, n < p.dstate);
-            load_frag<T>(q[I], qrow[I] + n, n < p.dstate);
-        }
+    for (int kb = 0; kb < NB; ++kb) {
+        if (32 * NB > p.dstate && 32 * kb + 8 * g >= p.dstate)
 #pragma unroll
-        for (int I = 0; I < 2; ++I) {
-            ksq[I] = squares(k[I], ksq[I]);
-            qsq[I] = squares(q[I], qsq[I]);
-        }
+            for (int I = 0; I < 2; ++I) {
+                kf[kb][I].zero();
+                qf[kb][I].zero();
+            }
+        const Frag<T>(&k)[2] = kf[kb];
+        const Frag<T>(&q)[2] = qf[kb];
         mma(k[0], k[0], kk[0]);
         mma(k[0], k[1], kk[1]);
         mma(k[1], k[1], kk[2]);
         mma(k[0], q[0], qk[0]);
         mma(k[0], q[1], qk[1]);
         mma(k[1], q[1], qk[2]);
+        if (p.l2norm)
+#pragma unroll
+            for (int I = 0; I < 2; ++I) {
+                ksq[I] = squares(k[I], ksq[I]);
+                qsq[I] = squares(q[I], qsq[I]);
+            }
     }
 #pragma unroll
     for (int I = 0; I < 2; ++I) {
+        float kr = 1.0f, qr = p.scale;
+        if (p.l2norm) {
 #pragma unroll
-        for (int m = 16; m < 64; m <<= 1) {
-            ksq[I] += __shfl_xor(ksq[I], m);
-            qsq[I] += __shfl_xor(qsq[I], m);
+            for (int m = 16; m < 64; m <<= 1) {
+                ksq[I] += __shfl_xor(ksq[I], m);
+                qsq[I] += __shfl_xor(qsq[I], m);
+            }
+            kr = 1.0f / sqrtf(ksq[I] + kNormEps);
+            qr *= 1.0f / sqrtf(qsq[I] + kNormEps);
         }
         if (g == 0) {
-            w.kr[16 * I + i16] = p.l2norm ? 1.0f / sqrtf(ksq[I] + kNormEps) : 1.0f;
-            w.qr[16 * I + i16] = p.l2norm ? p.scale * (1.0f / sqrtf(qsq[I] + kNormEps)) : p.scale;
+            w.kr[16 * I + i16] = kr;
+            w.qr[16 * I + i16] = qr;
         }
     }
-    __syncthreads();
+    wave_sync();
 
     // A and Pm.
     float pm[3][4];
-    f32x4 a10;
+    f32x4 a10, bj[2];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        const int I = (k + 1) / 2, J = k / 2, i = 16 * I + i16;
-        const double ci = w.cs2[i];
+        const int I = (k + 1) / 2, J = k / 2, i = 16 * I + i16, j0 = 16 * J + 4 * g;
+        const TwoFloats ci = {w.hi[i], w.lo[i]};
         const float bi = w.beta[i] * w.kr[i], qi = w.qr[i];
+        const f32x4 hj = *reinterpret_cast<const f32x4 *>(&w.hi[j0]), lj = *reinterpret_cast<const f32x4 *>(&w.lo[j0]),
+                    kj = *reinterpret_cast<const f32x4 *>(&w.kr[j0]);
+        bj[J] = *reinterpret_cast<const f32x4 *>(&w.beta[j0]);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int j = 16 * J + 4 * g + r;
-            const float e = exp2_f64(ci - w.cs2[j]) * w.kr[j];
-            pm[k][r] = j <= i ? qi * e * qk[k][r] : 0.0f;
-            const float a = j < i ? bi * e * kk[k][r] : 0.0f;
+            const float e = exp2_diff(ci, {hj[r], lj[r]}) * kj[r];
+            pm[k][r] = j0 + r <= i ? qi * e * qk[k][r] : 0.0f;
+            const float a = j0 + r < i ? bi * e * kk[k][r] : 0.0f;
             if (k == 1) a10[r] = a;
             else w.at[I][4 * g + r][i16] = a;
         }
     }
-    __syncthreads();
+    wave_sync();
     {
         const int blk = g & 1;
         float t[16];
 #pragma unroll
         for (int j = 15; j >= 0; --j) {
-            float s = 0.0f;
+            float s = j == i16 ? 1.0f : 0.0f;
 #pragma unroll
-            for (int m = 15; m > j; --m) s = fmaf(t[m], w.at[blk][j][m], s);
-            t[j] = (j == i16 ? 1.0f : 0.0f) - s;
+            for (int m = 15; m > j; --m) s = fmaf(-t[m], w.at[blk][j][m], s);
+            t[j] = s;
         }
         if (g < 2)
 #pragma unroll
             for (int j = 0; j < 16; j += 4)
                 *reinterpret_cast<f32x4 *>(&w.tb[blk][i16][j]) = f32x4{t[j], t[j + 1], t[j + 2], t[j + 3]};
     }
-    __syncthreads();
+    wave_sync();
     f32x4 tt[3];
     tt[0] = *reinterpret_cast<const f32x4 *>(&w.tb[0][i16][4 * g]);
     tt[2] = *reinterpret_cast<const f32x4 *>(&w.tb[1][i16][4 * g]);
@@ -272,14 +307,14 @@ __global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) tt[1][r] = -joined[r];
 
-    if (mine >= items) return;
     typedef Pack32<T> L;
-    char *out = p.pack + ((b * p.nheads + h) * p.nchunks + c) * L::kBytes;
+    const int64_t bh = (int64_t)b * p.nheads + h;
+    char *out = p.pack + (bh * p.nchunks + c) * L::kBytes;
     float tv[3][4];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) tv[k][r] = tt[k][r] * w.beta[16 * (k / 2) + 4 * g + r];
+        for (int r = 0; r < 4; ++r) tv[k][r] = tt[k][r] * bj[k / 2][r];
     auto put = [&](const float (&lo)[4], const float (&hi)[4], int off, auto terms) {
         constexpr int N = decltype(terms)::value;
         const float both[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
@@ -301,20 +336,20 @@ __global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
     put(pm[1], pm[2], L::kP1, std::integral_constant<int, kOut<T>>{});
     float *tab = reinterpret_cast<float *>(out + L::kTab);
     if (lane < C) {
-        const double cs = w.cs2[lane], end = w.cs2[C - 1];
-        const float e = exp2_f64(cs);
-        tab[L::kA + lane] = e * w.kr[lane];
+        const TwoFloats zero = {0.f, 0.f}, end = {w.hi[C - 1], w.lo[C - 1]};
+        const float e = exp2_diff(mine, zero), kr = w.kr[lane];
+        tab[L::kA + lane] = e * kr;
         tab[L::kC + lane] = e * w.qr[lane];
-        tab[L::kD + lane] = exp2_f64(end - cs) * w.kr[lane];
-        if (lane == 0) tab[L::kEnd] = exp2_f64(end);
+        tab[L::kD + lane] = exp2_diff(end, mine) * kr;
+        if (lane == 0) tab[L::kEnd] = exp2_diff(end, zero);
     }
     if (p.state_out) {
-        const int64_t at = min(max((int64_t)p.state_out_idx[b], (int64_t)-1), p.seqlen - 1);
-        if (at >= t0 && at < t0 + C && lane < C) {
-            float *to = p.at_tables + (b * p.nheads + h) * kAtFloats;
-            const double ce = w.cs2[(int)(at - t0)];
-            to[lane] = lane <= (int)(at - t0) ? exp2_f64(ce - w.cs2[lane]) * w.kr[lane] : 0.0f;
-            if (lane == 0) to[C] = exp2_f64(ce);
+        const int64_t at = min(max((int64_t)p.state_out_idx[b], (int64_t)-1), p.seqlen - 1) - t0;
+        if (at >= 0 && at < C && lane < C) {
+            float *to = p.at_tables + bh * kAtFloats;
+            const TwoFloats ce = {w.hi[(int)at], w.lo[(int)at]};
+            to[lane] = lane <= (int)at ? exp2_diff(ce, mine) * w.kr[lane] : 0.0f;
+            if (lane == 0) to[C] = exp2_diff(ce, {0.f, 0.f});
         }
     }
 }
@@ -792,10 +827,14 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 }
 
 template <typename T, int NB>
-hipError_t launch_chunks(const DeltaParams &p, hipStream_t stream) {
+hipError_t launch(const DeltaParams &p, hipStream_t stream) {
     constexpr int kLds = 160 * 1024;
     constexpr int BUFS = 2 * sizeof(Buffer<T, NB>) <= kLds ? 2 : 1;
     static_assert(BUFS * sizeof(Buffer<T, NB>) <= kLds, "LDS");
+    const int64_t waves = p.batch * p.nchunks * p.nheads;
+    delta_prepare<T, NB><<<(unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
+    const hipError_t r = hipGetLastError();
+    if (r != hipSuccess) return r;
     const int64_t items = p.batch * p.nheads * ((p.headdim + kSlice - 1) / kSlice);
     constexpr int WAVES = 2 * BUFS * sizeof(Buffer<T, NB>) <= kLds && NB <= 5 ? 2 : 1;
     if constexpr (sizeof(T) == 2) {
@@ -817,19 +856,15 @@ hipError_t launch_chunks(const DeltaParams &p, hipStream_t stream) {
 
 template <typename T>
 hipError_t run(const DeltaParams &p, hipStream_t stream) {
-    const int64_t waves = p.batch * p.nchunks * p.nheads;
-    delta_prepare<T><<<(unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
-    const hipError_t r = hipGetLastError();
-    if (r != hipSuccess) return r;
     switch ((p.dstate + 31) / 32) {
-        case 1: return launch_chunks<T, 1>(p, stream);
-        case 2: return launch_chunks<T, 2>(p, stream);
-        case 3: return launch_chunks<T, 3>(p, stream);
-        case 4: return launch_chunks<T, 4>(p, stream);
-        case 5: return launch_chunks<T, 5>(p, stream);
-        case 6: return launch_chunks<T, 6>(p, stream);
-        case 7: return launch_chunks<T, 7>(p, stream);
-        default: return launch_chunks<T, 8>(p, stream);
+        case 1: return launch<T, 1>(p, stream);
+        case 2: return launch<T, 2>(p, stream);
+        case 3: return launch<T, 3>(p, stream);
+        case 4: return launch<T, 4>(p, stream);
+        case 5: return launch<T, 5>(p, stream);
+        case 6: return launch<T, 6>(p, stream);
+        case 7: return launch<T, 7>(p, stream);
+        default: return launch<T, 8>(p, stream);
     }
 }
 
