@@ -149,9 +149,10 @@ struct DeltaParams {
     int nheads, headdim, dstate, ngroups, heads_per_group;
     float scale;
     int l2norm;
-    // Chunked form only, in the workspace: delta_pack_bytes per (b, h, chunk) and
+    // Chunked form only, in the workspace: delta_pack_bytes per (b, chunk, h) and
     // delta_at_bytes per (b, h).
     int64_t nchunks;
+    int prepare_heads;  // heads of a group per wave of the preparation
     char *pack;
     float *at_tables;
 };
