@@ -42,7 +42,7 @@ ssd_status check_delta(const ssd_delta_shape *s, ssd_dtype dtype) {
     return SSD_OK;
 }
 
-ssd::DeltaParams delta_params(const ssd_delta_shape *s) {
+ssd::DeltaParams delta_params(const ssd_delta_shape *s, ssd_dtype dtype) {
     ssd::DeltaParams p = {};
     p.batch = s->batch;
     p.seqlen = s->seqlen;
@@ -62,17 +62,27 @@ ssd::DeltaParams delta_params(const ssd_delta_shape *s) {
     p.beta_bs = used_stride(s->batch, s->beta_batch_stride);
     p.beta_ts = used_stride(s->seqlen, s->beta_token_stride);
     p.nchunks = s->seqlen > kDeltaTokens ? (s->seqlen + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk : 0;
+    ssd::delta_ranges(p, elem(dtype));
     return p;
 }
 
-// Byte offset of the accepted index's tables behind the chunks', and all.
+// Byte offsets behind the chunks' packs: the accepted index's tables, the ranges'
+// states, maps and copy of init_state.
 struct DeltaWorkspace {
-    size_t at_off, total;
+    size_t at_off, state_off, map_off, init_off, total;
 };
 DeltaWorkspace delta_workspace(const ssd::DeltaParams &p, ssd_dtype dtype) {
-    if (p.nchunks == 0) return {0, 0};
-    const size_t bh = (size_t)p.batch * p.nheads, packs = bh * p.nchunks * ssd::delta_pack_bytes(elem(dtype));
-    return {packs, packs + bh * ssd::delta_at_bytes()};
+    if (p.nchunks == 0) return {};
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const size_t bh = (size_t)p.batch * p.nheads, state = bh * p.headdim * p.dstate * sizeof(float),
+                 map = bh * p.dstate * p.dstate * sizeof(float), more = p.ranges > 1 ? p.ranges - 1 : 0;
+    DeltaWorkspace w = {};
+    w.at_off = up(bh * p.nchunks * ssd::delta_pack_bytes(elem(dtype)));
+    w.state_off = w.at_off + up(bh * ssd::delta_at_bytes());
+    w.map_off = w.state_off + up(more * state);
+    w.init_off = w.map_off + up(more > 0 ? (more - 1) * map : 0);
+    w.total = w.init_off + (more > 0 ? state : 0);
+    return w;
 }
 
 }  // namespace
@@ -81,7 +91,7 @@ extern "C" {
 
 size_t ssd_gated_delta_workspace_bytes(const ssd_delta_shape *shape, ssd_dtype dtype) {
     if (check_delta(shape, dtype) != SSD_OK) return 0;
-    return delta_workspace(delta_params(shape), dtype).total;
+    return delta_workspace(delta_params(shape, dtype), dtype).total;
 }
 
 ssd_status ssd_gated_delta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
@@ -104,7 +114,7 @@ ssd_status ssd_gated_delta_fwd(const void *q, const void *k, const void *v, cons
     if (!isfinite(scale)) return fail(SSD_ERR_ARGS, "scale must be finite");
     if (b > 0 && T > 0 && (!q || !k || !v || !beta || !y))
         return fail(SSD_ERR_NULL, "q, k, v, beta and y are required");
-    ssd::DeltaParams p = delta_params(s);
+    ssd::DeltaParams p = delta_params(s, dtype);
     const DeltaWorkspace ws = delta_workspace(p, dtype);
     const size_t ws_need = ws.total;
     if (ws_need > 0 && !workspace) return fail(SSD_ERR_WORKSPACE, "workspace is NULL");
@@ -142,6 +152,9 @@ ssd_status ssd_gated_delta_fwd(const void *q, const void *k, const void *v, cons
     if (p.nchunks == 0) return launched("gated_delta", ssd::launch_delta_tokens(p, elem(dtype), stream));
     p.pack = static_cast<char *>(workspace);
     p.at_tables = reinterpret_cast<float *>(p.pack + ws.at_off);
+    p.range_state = reinterpret_cast<float *>(p.pack + ws.state_off);
+    p.range_map = reinterpret_cast<float *>(p.pack + ws.map_off);
+    p.range_init = reinterpret_cast<float *>(p.pack + ws.init_off);
     return launched("gated_delta", ssd::launch_delta_chunks(p, elem(dtype), stream));
 }
 

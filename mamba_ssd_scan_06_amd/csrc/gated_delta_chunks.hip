@@ -27,6 +27,8 @@
 // three.  Where the result is only rounded to a bf16 output (S q and Pm U of bf16
 // calls), two terms (16 bits) are taken: 2^-16 beside the output's 2^-8.  This is
 // 3 to 6 products of the bf16 rate, which is 16 times the fp32 rate.
+#include <math.h>
+
 #include "device_common.hpp"
 #include "kernels.hpp"
 
@@ -403,8 +405,12 @@ struct Carry {
 // WAVES: waves per SIMD to leave registers for (two keep the accumulators in
 // the ordinary registers too).  DIRECT: bf16 rows of 16-byte alignment, which the
 // buffer loads that write LDS by themselves take; other rows pass through
-// registers.
-template <typename T, int NB, int BUFS, int WAVES, bool DIRECT>
+// registers.  OUT: outputs are computed (and the chunks of one range are walked
+// from its entering state); without, the first pass over the ranges: each leaves
+// its final state from a zero start (the first one from init_state) and, in
+// further slices of rows that start as the unit matrix with v = 0, the map M of
+// the state that enters it (S_end = S_begin M + that final state).
+template <typename T, int NB, int BUFS, int WAVES, bool DIRECT, bool OUT>
 __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     typedef Pack32<T> L;
     typedef Buffer<T, NB> Buf;
@@ -420,18 +426,29 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     // Consecutive items (the slices of a head, the heads of a group) on one XCD.
     const unsigned xcd = blockIdx.x % 8, whole = gridDim.x / 8, more = gridDim.x % 8;
     const unsigned item = xcd * whole + min(xcd, more) + blockIdx.x / 8;
-    const int slices = (p.headdim + kSlice - 1) / kSlice;
-    const unsigned bh = item / (unsigned)slices, b = bh / (unsigned)p.nheads, h = bh - b * (unsigned)p.nheads;
-    const int slice0 = (int)(item - bh * (unsigned)slices) * kSlice;
+    // An item is a slice of rows of a (sequence, range, head), in this order.
+    const int v_slices = (p.headdim + kSlice - 1) / kSlice;
+    const int slices = OUT ? v_slices : v_slices + (p.dstate + kSlice - 1) / kSlice;
+    const unsigned brh = item / (unsigned)slices, br = brh / (unsigned)p.nheads, h = brh - br * (unsigned)p.nheads;
+    const unsigned ranges = (unsigned)(OUT ? p.ranges : p.ranges - 1), b = br / ranges, range = br - b * ranges;
+    const unsigned bh = b * (unsigned)p.nheads + h;
+    const int slice = (int)(item - brh * (unsigned)slices);
+    const bool map = !OUT && slice >= v_slices;
+    if (map && range == 0) return;  // nothing enters the first range but init_state
+    const int slice0 = (map ? slice - v_slices : slice) * kSlice, all_rows = map ? p.dstate : p.headdim;
+    // This range's tokens: the first, and how many.
+    const int64_t first = (int64_t)range * p.range_chunks * C;
+    const int tokens = (int)min(p.range_chunks * C, p.seqlen - first);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, g = lane >> 4;
     const int N = p.dstate, p0 = slice0 + 16 * wave;
-    const bool live = p0 < p.headdim;  // whole waves only: headdim is a multiple of 16
+    const bool live = p0 < all_rows;  // whole waves only: both sizes are multiples of 16
     const int group = (int)h / p.heads_per_group;
 
-    const T *kbase = reinterpret_cast<const T *>(p.k) + b * p.k_bs + (int64_t)group * N;
-    const T *qbase = reinterpret_cast<const T *>(p.q) + b * p.q_bs + (int64_t)group * N;
-    const T *vbase = reinterpret_cast<const T *>(p.v) + b * p.v_bs + (int64_t)h * p.headdim + slice0;
-    const char *packs = p.pack + ((int64_t)b * p.nchunks * p.nheads + h) * L::kBytes;
+    const T *kbase = reinterpret_cast<const T *>(p.k) + b * p.k_bs + first * p.k_ts + (int64_t)group * N;
+    const T *qbase = reinterpret_cast<const T *>(p.q) + b * p.q_bs + first * p.q_ts + (int64_t)group * N;
+    const T *vbase = reinterpret_cast<const T *>(p.v) + b * p.v_bs + first * p.v_ts + (int64_t)h * p.headdim + (map ? 0 : slice0);
+    const int v_cols = map ? 0 : min(kSlice, p.headdim - slice0);  // a map has no v: zeros
+    const char *packs = p.pack + (((int64_t)b * p.nchunks + first / C) * p.nheads + h) * L::kBytes;
     const int64_t pack_stride = (int64_t)p.nheads * L::kBytes;
     // Direct copies: a wave instruction fills 64 consecutive 16-byte pieces of
     // LDS, each lane from an offset of its own into the chunk's rows.  Columns
@@ -444,7 +461,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     // cycles of a chunk).  Nothing branches: the last chunk's copies of a chunk
     // that is not there read an empty buffer.
     const int uwave = __builtin_amdgcn_readfirstlane(wave);
-    constexpr int kSteps = NB + 3;
+    constexpr int kKeySteps = OUT ? NB : (NB + 1) / 2, kSteps = kKeySteps + 3;
     uint32_t kq_off[NB], v_off;
     auto is_query = [&](int k) { return 4 * k + uwave >= 2 * NB; };
     if constexpr (DIRECT) {
@@ -455,26 +472,36 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             kq_off[k] = n < N ? 2u * ((uint32_t)row * (uint32_t)(is_query(k) ? p.q_ts : p.k_ts) + (uint32_t)n) : 0xffffff00u;
         }
         const int at = 64 * uwave + lane, row = at / 8, n = 8 * ((at % 8) ^ v_swz<T>(row));
-        v_off = n < min(kSlice, p.headdim - slice0) ? 2u * ((uint32_t)row * (uint32_t)p.v_ts + (uint32_t)n) : 0xffffff00u;
+        v_off = n < v_cols ? 2u * ((uint32_t)row * (uint32_t)p.v_ts + (uint32_t)n) : 0xffffff00u;
     }
-    auto copy = [&](const void *base, int rows, int64_t ts, int inner, uint32_t off, void *to) {
-        const uint32_t bytes = rows > 0 ? 2u * (uint32_t)((rows - 1) * (int)ts + inner) : 0u;
+    // The next chunk's rows, and the tokens from it on (none or fewer: no chunk).
+    const T *k_next = kbase, *q_next = qbase, *v_next = vbase;
+    const char *pack_next = packs;
+    int left_next = tokens;
+    auto copy = [&](const void *base, uint32_t bytes, uint32_t off, void *to) __attribute__((always_inline)) {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(base, bytes), (__attribute__((address_space(3))) void *)to, 16,
                                                  (int)off, 0, 0, 0);
     };
-    auto fetch_step = [&](int64_t c, int k, Buf &to) __attribute__((always_inline)) {
-        const int rows = (int)max(min(p.seqlen - c * C, (int64_t)C), (int64_t)0);
-        if (k < NB) {
+    auto fetch_step = [&](int k, Buf &to) __attribute__((always_inline)) {
+        const uint32_t before = (uint32_t)min(left_next, C) - 1u;  // rows before the last
+        auto bytes = [&](int64_t ts, int inner) { return left_next > 0 ? 2u * (before * (uint32_t)ts + (uint32_t)inner) : 0u; };
+        if (k < kKeySteps) {
             const bool q = is_query(k);
-            const int64_t ts = q ? p.q_ts : p.k_ts;
-            copy((q ? qbase : kbase) + c * C * ts, rows, ts, N, kq_off[k],
+            copy(q ? q_next : k_next, bytes(q ? p.q_ts : p.k_ts, N), kq_off[k],
                  q ? &to.q[0][0][0] + 512 * (4 * k + uwave - 2 * NB) : &to.k[0][0][0] + 512 * (4 * k + uwave));
-        } else if (k == NB) {
-            copy(vbase + c * C * p.v_ts, rows, p.v_ts, min(kSlice, p.headdim - slice0), v_off, &to.v[0][0] + 512 * uwave);
+        } else if (k == kKeySteps) {
+            copy(v_next, map ? 0u : bytes(p.v_ts, v_cols), v_off, &to.v[0][0] + 512 * uwave);
         } else {
-            const int at = 1024 * (4 * (k - NB - 1) + uwave);
-            copy(packs + c * pack_stride, min(rows, 1), 0, L::kBytes / 2, (uint32_t)at + 16u * lane, to.pack + at);
+            const int at = 1024 * (4 * (k - kKeySteps - 1) + uwave);
+            copy(pack_next, left_next > 0 ? (uint32_t)L::kBytes : 0u, (uint32_t)at + 16u * lane, to.pack + at);
         }
+    };
+    auto advance = [&]() __attribute__((always_inline)) {
+        k_next += C * p.k_ts;
+        q_next += C * p.q_ts;
+        v_next += C * p.v_ts;
+        pack_next += pack_stride;
+        left_next -= C;
     };
     // Through registers: eight elements per piece; rows past the end repeat the last one (their u
     // are 0), columns past N are 0.  A thread's pieces keep their rows and
@@ -489,20 +516,20 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         row = piece / (4 * NB);
         n = 8 * (piece % (4 * NB));
     };
-    auto point = [&](int64_t c) {
-        const int left = (int)min(p.seqlen - c * C, (int64_t)C) - 1;  // the last row
+    auto point = [&]() {  // at the next chunk
+        const int left = min(left_next, C) - 1;  // the last row
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             bool is_q;
             int row, n;
             piece_of(i, is_q, row, n);
-            const int64_t t = c * C + min(row, left);
-            kq_at[i] = (is_q ? qbase + t * p.q_ts : kbase + t * p.k_ts) + min(n, N - 8);
+            const int64_t t = min(row, left);
+            kq_at[i] = (is_q ? q_next + t * p.q_ts : k_next + t * p.k_ts) + min(n, N - 8);
         }
-        v_at = vbase + (c * C + min(v_row, left)) * p.v_ts + min(v_col, p.headdim - slice0 - 8);
+        v_at = v_next + (int64_t)min(v_row, left) * p.v_ts + min(v_col, max(v_cols, 8) - 8);
     };
-    auto fetch = [&](Regs &r, int64_t c, Buf &to) __attribute__((always_inline)) {
-        if (c + 1 == p.nchunks && c > 0) point(c);
+    auto fetch = [&](Regs &r, Buf &to) __attribute__((always_inline)) {
+        if (left_next < C) point();
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
 #pragma unroll
@@ -515,7 +542,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 #pragma unroll
         for (int j = 0; j < Regs::WORDS; ++j) r.v[j] = load_words(v_at + j * Regs::VEC);
         v_at += C * p.v_ts;
-        const char *src = packs + c * pack_stride;
+        const char *src = pack_next;
         if constexpr (BUFS == 2) {
             // The other buffer's last reader is behind the last barrier.
 #pragma unroll
@@ -552,7 +579,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         }
 #pragma unroll
         for (int j = 0; j < Regs::WORDS; ++j)
-            *reinterpret_cast<u32x4 *>(&to.v[v_row][(v_col ^ 8 * v_swz<T>(v_row)) + j * Regs::VEC]) = r.v[j];
+            *reinterpret_cast<u32x4 *>(&to.v[v_row][(v_col ^ 8 * v_swz<T>(v_row)) + j * Regs::VEC]) =
+                map ? u32x4{0u, 0u, 0u, 0u} : r.v[j];
         if constexpr (BUFS == 1)
 #pragma unroll
             for (int i = 0; i < Regs::kPackWords; ++i)
@@ -562,7 +590,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     // Tile (kb, half) of the state: rows n = 32 kb + 8 g + 4 half + r, column p0 +
     // i16; the two halves' eight rows of a lane are consecutive.
     f32x4 s[NB][2];
-    const int64_t s_off = ((int64_t)bh * p.headdim + (live ? p0 : 0) + i16) * N + 8 * g;
+    const int64_t s_off = (int64_t)((live ? p0 : 0) + i16) * N + 8 * g, v_state = (int64_t)p.headdim * N;
     auto store_state = [&](const f32x4 (&m)[NB][2], float *to) {
         if (!live) return;
 #pragma unroll
@@ -572,18 +600,29 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 *reinterpret_cast<f32x4 *>(to + s_off + 32 * kb + 4) = m[kb][1];
             }
     };
+    // Of range r, [range][b,h][P,N]: its final state, later the state that enters
+    // range r + 1.
+    auto range_state = [&](unsigned r) { return p.range_state + ((int64_t)r * p.batch * p.nheads + bh) * v_state; };
+    const float *from = nullptr;
+    if (OUT && range > 0) from = range_state(range - 1);
+    else if (OUT && p.ranges > 1) from = p.init_state ? p.range_init + bh * v_state : nullptr;
+    else if (range == 0 && p.init_state) from = p.init_state + bh * v_state;
 #pragma unroll
     for (int kb = 0; kb < NB; ++kb) {
         s[kb][0] = s[kb][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (p.init_state && 32 * kb + 8 * g < N) {
-            s[kb][0] = *reinterpret_cast<const f32x4 *>(p.init_state + s_off + 32 * kb);
-            s[kb][1] = *reinterpret_cast<const f32x4 *>(p.init_state + s_off + 32 * kb + 4);
+        if (from && 32 * kb + 8 * g < N) {
+            s[kb][0] = *reinterpret_cast<const f32x4 *>(from + s_off + 32 * kb);
+            s[kb][1] = *reinterpret_cast<const f32x4 *>(from + s_off + 32 * kb + 4);
         }
+        if (map)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[kb][i >> 2][i & 3] = 32 * kb + 8 * g + i == p0 + i16 ? 1.0f : 0.0f;
     }
-    int64_t at = -2;  // the accepted index
-    if (p.state_out) {
-        at = min(max((int64_t)p.state_out_idx[b], (int64_t)-1), p.seqlen - 1);
-        if (at < 0) store_state(s, p.state_out);
+    int at = -1;  // the accepted index within this range, none of its own below 0
+    if (OUT && p.state_out) {
+        const int64_t j = min(max((int64_t)p.state_out_idx[b], (int64_t)-1), p.seqlen - 1);
+        if (j < 0 && range == 0) store_state(s, p.state_out + bh * v_state);
+        at = j >= first && j < first + tokens ? (int)(j - first) : -1;
     }
 
     // K' of a chunk as an operand with rows n of tile (kb, half) and the tokens
@@ -608,27 +647,30 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     Regs regs;
     if constexpr (DIRECT) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) fetch_step(0, k, buf0);
+        for (int k = 0; k < kSteps; ++k) fetch_step(k, buf0);
     } else {
-        point(0);
-        fetch(regs, 0, buf0);
+        point();
+        fetch(regs, buf0);
         place(regs, buf0);
     }
+    advance();
     // Outputs by a buffer over the chunk's rows, which drops those past the end.
     const uint32_t y_row = (uint32_t)(p.nheads * p.headdim * (int)sizeof(T));
     const uint32_t y_off = (uint32_t)i16 * y_row + (uint32_t)(((int)h * p.headdim + p0 + 4 * g) * (int)sizeof(T));
     wait_vmcnt<0>();
     __syncthreads();
-    const int64_t nc = p.nchunks;
-    // One chunk from `buf`, while the next one comes into `other`.
-    auto chunk = [&](int64_t c, const Buf &buf, Buf &other) __attribute__((always_inline)) {
-        if (!DIRECT && c + 1 < nc) fetch(regs, c + 1, other);
+    char *y_at = reinterpret_cast<char *>(p.y) + ((int64_t)b * p.seqlen + first) * (int64_t)y_row;
+    // The chunk whose first token is `t` from `buf`, while the next one comes into
+    // `other`.
+    auto chunk = [&](int t, const Buf &buf, Buf &other) __attribute__((always_inline)) {
+        const bool more = left_next > 0;
+        if (!DIRECT && more) fetch(regs, other);
         // A wave without rows issues its copies at once.
         auto fetch_some = [&](int from, int to) {
             if constexpr (DIRECT)
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k)
-                    if (k >= from && k < to) fetch_step(c + 1, k, other);
+                    if (k >= from && k < to) fetch_step(k, other);
         };
         if (!live) fetch_some(0, kSteps);
         f32x4 qs[2] = {};  // S q, then y
@@ -654,8 +696,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 if (kb + 1 < NB) rows_of(buf.k, kb + 1, kf[(kb + 1) & 1]);
-                else rows_of(buf.q, 0, qf[0]);
-                fetch_some(kb, kb + 1);
+                else if (OUT) rows_of(buf.q, 0, qf[0]);
+                if (kb < kKeySteps) fetch_some(kb, kb + 1);
                 __builtin_amdgcn_sched_barrier(0);
                 float f[8];
 #pragma unroll
@@ -668,11 +710,12 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 for (int I = 0; I < 2; ++I) mma_terms<NI, 3>(kf[kb & 1][I], st, ks[I]);
             }
             auto s_q = [&](int kb) {
-                if (kb + 1 < NB) rows_of(buf.q, kb + 1, qf[(kb + 1) & 1]);
-                fetch_some(NB + (kb == 0 ? 0 : kb + 1), kb + 1 == NB ? kSteps : NB + kb + 2);
+                if (OUT && kb + 1 < NB) rows_of(buf.q, kb + 1, qf[(kb + 1) & 1]);
+                fetch_some(kKeySteps + (kb == 0 ? 0 : kb + 1), kb + 1 == NB ? kSteps : kKeySteps + kb + 2);
                 __builtin_amdgcn_sched_barrier(0);
+                if (OUT)
 #pragma unroll
-                for (int I = 0; I < 2; ++I) mma_terms<NO, NI>(sf[kb], qf[kb & 1][I], qs[I]);
+                    for (int I = 0; I < 2; ++I) mma_terms<NO, NI>(sf[kb], qf[kb & 1][I], qs[I]);
             };
             // X = v - a S k.
             f32x4 av[2];
@@ -726,7 +769,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             }
             const float end = tab[L::kEnd];
             __builtin_amdgcn_sched_barrier(0);
-            if (at >= c * C && at < c * C + C) {  // the state after the accepted index
+            if (at >= t && at - t < C) {  // the state after the accepted index
                 const float *wt = p.at_tables + (int64_t)bh * kAtFloats;
                 const float e = wt[C];
                 float uv[8];
@@ -745,7 +788,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                         for (int r = 0; r < 4; ++r) m[kb][half][r] = s[kb][half][r] * e;
                         mma_terms<NI, 3>(kt, uf, m[kb][half]);
                     }
-                store_state(m, p.state_out);
+                store_state(m, p.state_out + bh * v_state);
             }
             // The state after the chunk.
             {
@@ -780,7 +823,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 }
             }
             // y: rows p = p0 + 4 g + r, column: token 16 I + i16.
-            {
+            if constexpr (OUT) {
                 float uv[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3];
@@ -801,41 +844,80 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         // stored: the counter would make the wait include the stores.
         if (BUFS == 2) wait_vmcnt<0>();  // among them the copies into the other buffer
         else __syncthreads();            // the only buffer is read no more
-        if (!DIRECT && c + 1 < nc) place(regs, other);
+        if (!DIRECT && more) place(regs, other);
         __builtin_amdgcn_sched_barrier(0);
-        if (live)
+        if (OUT && live)
 #pragma unroll
             for (int I = 0; I < 2; ++I) {
                 if constexpr (DIRECT) {
-                    const uint32_t rows = (uint32_t)min(p.seqlen - c * C, (int64_t)C);
-                    const __amdgpu_buffer_rsrc_t yr = buffer_rsrc(
-                        reinterpret_cast<char *>(p.y) + ((int64_t)b * p.seqlen + c * C) * (int64_t)y_row, rows * y_row);
+                    const __amdgpu_buffer_rsrc_t yr = buffer_rsrc(y_at, (uint32_t)min(tokens - t, C) * y_row);
                     const bf16x4 o = {(bf16)qs[I][0], (bf16)qs[I][1], (bf16)qs[I][2], (bf16)qs[I][3]};
                     __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, o), yr, (int)(y_off + 16u * I * y_row), 0, 0);
-                } else {
-                    const int64_t t = c * C + 16 * I + i16;
-                    T *to = reinterpret_cast<T *>(p.y) + (((int64_t)b * p.seqlen + t) * p.nheads + h) * p.headdim + p0 + 4 * g;
-                    if (t < p.seqlen) {
-                        if constexpr (sizeof(T) == 2) {
-                            const bf16x4 o = {(bf16)qs[I][0], (bf16)qs[I][1], (bf16)qs[I][2], (bf16)qs[I][3]};
-                            *reinterpret_cast<u32x2_at2 *>(to) = __builtin_bit_cast(u32x2, o);
-                        } else {
-                            store_words(to, __builtin_bit_cast(u32x4, qs[I]));
-                        }
+                } else if (16 * I + i16 < tokens - t) {
+                    T *to = reinterpret_cast<T *>(y_at + (int64_t)(16 * I + i16) * y_row) + (int64_t)h * p.headdim + p0 + 4 * g;
+                    if constexpr (sizeof(T) == 2) {
+                        const bf16x4 o = {(bf16)qs[I][0], (bf16)qs[I][1], (bf16)qs[I][2], (bf16)qs[I][3]};
+                        *reinterpret_cast<u32x2_at2 *>(to) = __builtin_bit_cast(u32x2, o);
+                    } else {
+                        store_words(to, __builtin_bit_cast(u32x4, qs[I]));
                     }
                 }
             }
+        y_at += (int64_t)C * y_row;
+        advance();
         __syncthreads();
     };
     if constexpr (BUFS == 2) {
-        for (int64_t c = 0; c < nc; c += 2) {
-            chunk(c, buf0, buf1);
-            if (c + 1 < nc) chunk(c + 1, buf1, buf0);
+        for (int left = tokens; left > 0; left -= 2 * C) {
+            chunk(tokens - left, buf0, buf1);
+            if (left > C) chunk(tokens - left + C, buf1, buf0);
         }
     } else {
-        for (int64_t c = 0; c < nc; ++c) chunk(c, buf0, buf0);
+        for (int left = tokens; left > 0; left -= C) chunk(tokens - left, buf0, buf0);
     }
-    if (p.final_state) store_state(s, p.final_state);
+    if constexpr (OUT) {
+        if (p.final_state && range + 1 == ranges) store_state(s, p.final_state + bh * v_state);
+    } else {
+        if (map) store_state(s, p.range_map + ((int64_t)(range - 1) * p.batch * p.nheads + bh) * N * N);
+        else store_state(s, range_state(range));
+    }
+}
+
+// Between the passes: the states that enter the ranges, S_{r+1} = S_r M_r + D_r
+// one after the other, in place of the D_r.  A workgroup per (b, h, 16 rows), a
+// wave per 16 columns, fp32 products; S_r passes through LDS.  It also sets
+// init_state aside, which the last range may overwrite (in-place calls) before
+// the first one starts.
+constexpr int kJoinRow = 256 + 4;
+__global__ __launch_bounds__(1024) void delta_join(DeltaParams p) {
+    __shared__ __attribute__((aligned(16))) float held[16][kJoinRow];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, g = lane >> 4, N = p.dstate;
+    const unsigned tiles = (unsigned)p.headdim / 16, bh = blockIdx.x / tiles, tile = blockIdx.x - bh * tiles;
+    const int64_t BH = p.batch * p.nheads, v_state = (int64_t)p.headdim * N, mine = bh * v_state + (int64_t)tile * 16 * N;
+    if (p.init_state)
+        for (int i = 4 * tid; i < 16 * N; i += 4 * (int)blockDim.x)
+            *reinterpret_cast<f32x4 *>(p.range_init + mine + i) = *reinterpret_cast<const f32x4 *>(p.init_state + mine + i);
+    for (int i = 4 * tid; i < 16 * N; i += 4 * (int)blockDim.x)
+        *reinterpret_cast<f32x4 *>(&held[i / N][i % N]) = *reinterpret_cast<const f32x4 *>(p.range_state + mine + i);
+    __syncthreads();
+    const int n = 16 * wave + i16;  // this lane's column, rows 4 g + r
+    for (int r = 1; r + 1 < p.ranges; ++r) {
+        const float *m = p.range_map + ((int64_t)(r - 1) * BH + bh) * N * N + n;
+        float *d = p.range_state + (int64_t)r * BH * v_state + mine + n;
+        f32x4 acc;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = d[(4 * g + k) * N];
+        for (int k0 = 0; k0 < N; k0 += 16) {
+            f32x4 b;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b[k] = m[(int64_t)(k0 + 4 * g + k) * N];
+            acc = mma_f32_16(*reinterpret_cast<const f32x4 *>(&held[i16][k0 + 4 * g]), b, acc);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) held[4 * g + k][n] = d[(4 * g + k) * N] = acc[k];
+        __syncthreads();
+    }
 }
 
 template <typename T, int NB>
@@ -854,8 +936,22 @@ hipError_t launch(const DeltaParams &given, hipStream_t stream) {
     delta_prepare<T, NB><<<(unsigned)((waves + kThreads / 64 - 1) / (kThreads / 64)), kThreads, 0, stream>>>(p);
     const hipError_t r = hipGetLastError();
     if (r != hipSuccess) return r;
-    const int64_t items = p.batch * p.nheads * ((p.headdim + kSlice - 1) / kSlice);
+    const int64_t v_slices = (p.headdim + kSlice - 1) / kSlice, n_slices = (p.dstate + kSlice - 1) / kSlice;
+    const int64_t heads = p.batch * p.nheads;
     constexpr int WAVES = 2 * BUFS * sizeof(Buffer<T, NB>) <= kLds && NB <= 5 ? 2 : 1;
+    auto passes = [&](auto direct) {
+        constexpr bool D = decltype(direct)::value;
+        if (p.ranges > 1) {
+            delta_chunks<T, NB, BUFS, WAVES, D, false>
+                <<<(unsigned)(heads * (p.ranges - 1) * (v_slices + n_slices)), kThreads, 0, stream>>>(p);
+            hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            delta_join<<<(unsigned)(heads * (p.headdim / 16)), 64 * (p.dstate / 16), 0, stream>>>(p);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        delta_chunks<T, NB, BUFS, WAVES, D, true><<<(unsigned)(heads * p.ranges * v_slices), kThreads, 0, stream>>>(p);
+        return hipGetLastError();
+    };
     if constexpr (sizeof(T) == 2) {
         // Direct copies need rows of 16-byte alignment and 32-bit offsets within a
         // chunk (the last byte below 2^31, so that the mark of no element is out).
@@ -864,13 +960,10 @@ hipError_t launch(const DeltaParams &given, hipStream_t stream) {
         };
         const int64_t y_bytes = (int64_t)C * p.nheads * p.headdim * 2;
         if (fits(p.q, p.q_bs, p.q_ts, 256) && fits(p.k, p.k_bs, p.k_ts, 256) && fits(p.v, p.v_bs, p.v_ts, 256) &&
-            (uintptr_t)p.y % 16 == 0 && y_bytes < ((int64_t)1 << 31)) {
-            delta_chunks<T, NB, BUFS, WAVES, true><<<(unsigned)items, kThreads, 0, stream>>>(p);
-            return hipGetLastError();
-        }
+            (uintptr_t)p.y % 16 == 0 && y_bytes < ((int64_t)1 << 31))
+            return passes(std::true_type{});
     }
-    delta_chunks<T, NB, BUFS, WAVES, false><<<(unsigned)items, kThreads, 0, stream>>>(p);
-    return hipGetLastError();
+    return passes(std::false_type{});
 }
 
 template <typename T>
@@ -888,6 +981,42 @@ hipError_t run(const DeltaParams &p, hipStream_t stream) {
 }
 
 }  // namespace
+
+// Few heads leave most of the GPU idle while their chunks are walked one after
+// the other, so a long sequence is cut into ranges of chunks that run side by
+// side, twice (see delta_chunks), with a join between.  In units of a chunk's
+// time with one workgroup per compute unit, a pass over ranges of L chunks takes
+// L, 1.75 L where two workgroups share a unit, and as often that as the GPU has
+// to be filled; the first pass computes no outputs (0.8), and its workgroups are
+// more (the maps' rows); the launches and the join add about 5 + 0.6 per range.
+// Measured, 16384 tokens of 32 heads (N and P 128, bf16) in 1, 2, 3, 4, 6, 8 and
+// 10 ranges: 861, 791, 562, 501, 533, 505 and 575 us; 1021 tokens of 30 heads
+// (N 96, P 80, fp32: one workgroup per unit) in 1, 2, 3, 4 and 6: 105, 103, 87,
+// 99 and 133 us.
+void delta_ranges(DeltaParams &p, Elem e) {
+    p.ranges = 1;
+    p.range_chunks = p.nchunks;
+    if (p.nchunks < 2) return;
+    const double heads = (double)p.batch * p.nheads;
+    const int v_slices = (p.headdim + kSlice - 1) / kSlice, n_slices = (p.dstate + kSlice - 1) / kSlice;
+    const bool pairs = e == Elem::BF16 && p.dstate <= 160;  // two workgroups fit a compute unit
+    auto rounds = [&](double wgs) {
+        if (wgs <= 256.0) return 1.0;
+        return pairs ? 1.75 * ceil(wgs / 512.0) : ceil(wgs / 256.0);
+    };
+    double best = 0.9 * (double)p.nchunks * rounds(heads * v_slices);
+    for (int r = 2; r <= 16; ++r) {
+        const int64_t len = (p.nchunks + r - 1) / r;
+        if ((p.nchunks + len - 1) / len != r) continue;  // fewer ranges of this length
+        const double first = heads * (v_slices + (r - 2) * (v_slices + n_slices)), second = heads * v_slices * r;
+        const double cost = (double)len * (0.8 * rounds(first) + rounds(second)) + 5.0 + 0.6 * r;
+        if (cost < best) {
+            best = cost;
+            p.ranges = r;
+            p.range_chunks = len;
+        }
+    }
+}
 
 size_t delta_pack_bytes(Elem e) { return e == Elem::BF16 ? Pack32<bf16>::kBytes : Pack32<float>::kBytes; }
 size_t delta_at_bytes() { return kAtFloats * sizeof(float); }

@@ -155,7 +155,15 @@ struct DeltaParams {
     int prepare_heads;  // heads of a group per wave of the preparation
     char *pack;
     float *at_tables;
+    // Ranges of chunks (delta_ranges); with more than one, the workspace holds
+    // [ranges - 1][b,H,P,N] states, [ranges - 2][b,H,N,N] maps and a copy of
+    // init_state.
+    int ranges;
+    int64_t range_chunks;
+    float *range_state, *range_map, *range_init;
 };
+// Chooses ranges and range_chunks from the sizes.
+void delta_ranges(DeltaParams &p, Elem e);
 constexpr int kDeltaChunk = 32;  // tokens of a chunk
 // Token by token (any number of them), and in chunks with the workspace.
 hipError_t launch_delta_tokens(const DeltaParams &p, Elem e, hipStream_t stream);

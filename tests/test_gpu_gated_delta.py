@@ -111,6 +111,94 @@ def test_against_definition(case):
     check(inputs(1, b, T, H, P, N, G, dtype, init, idx, lead, pad, decay, unit=not l2), dtype, l2=l2)
 
 
+@pytest.mark.parametrize("dtype,lead", [("bf16", 0), ("bf16", 1), ("f32", 0)])
+@pytest.mark.parametrize("N", [16, 48, 80, 128, 144, 192, 208, 256])
+def test_many_heads(N, dtype, lead):
+    # More workgroups than compute units: the other split of the work.
+    announce(N, dtype, lead)
+    check(inputs(20, 9, 70, 32, 16, N, 8, dtype, lead=lead, unit=True), dtype)
+
+
+@pytest.mark.parametrize("dtype,lead", [("bf16", 0), ("bf16", 3), ("f32", 0)])
+def test_many_heads_several_slices(dtype, lead):
+    check(inputs(21, 5, 97, 32, 80, 128, 4, dtype, lead=lead), dtype, l2=True)
+
+
+def ranges_of(b, T, H, P, N, G, dtype):
+    """The number of token ranges a call is cut into, from the workspace: behind
+    the chunks' tables and the accepted indices' stand the ranges' states, maps
+    and a copy of init_state."""
+    code = ssd.SSD_DTYPE_BF16 if dtype == "bf16" else ssd.SSD_DTYPE_F32
+    need = ssd.ssd_gated_delta_workspace_bytes(ssd.ssd_delta_shape(b, T, H, P, N, G, *([0] * 10)), code)
+    up = lambda n: (n + 255) // 256 * 256
+    one = up(b * H * -(-T // 32) * (8192 if dtype == "bf16" else 9728)) + up(b * H * 144)
+    for r in range(2, 17):
+        if one + up(4 * (r - 1) * b * H * P * N) + up(4 * (r - 2) * b * H * N * N) + 4 * b * H * P * N == need:
+            return r
+    assert need == one
+    return 1
+
+
+RANGES = [
+    # b, T, H, P, N, G, dtype, init, lead
+    (1, 1300, 1, 16, 16, 1, "bf16", True, 0),
+    (2, 1111, 2, 80, 48, 1, "bf16", True, 1),
+    (1, 2100, 4, 128, 128, 2, "bf16", True, 0),
+    (1, 1500, 2, 256, 64, 2, "bf16", False, 0),
+    (1, 1200, 1, 64, 144, 1, "bf16", True, 0),
+    (1, 1025, 2, 32, 256, 1, "bf16", True, 0),
+    (1, 1025, 1, 48, 208, 1, "bf16", True, 8),
+    (1, 1300, 3, 16, 96, 3, "f32", True, 0),
+    (2, 1057, 2, 144, 128, 1, "f32", True, 3),
+    (1, 999, 1, 64, 256, 1, "f32", False, 0),
+]
+
+
+@pytest.mark.parametrize("case", RANGES, ids=["-".join(map(str, c)) for c in RANGES])
+def test_token_ranges(case):
+    b, T, H, P, N, G, dtype, init, lead = case
+    announce(*case)
+    r = ranges_of(b, T, H, P, N, G, dtype)
+    assert r >= 3
+    s = inputs(22, b, T, H, P, N, G, dtype, init=init, lead=lead)
+    s["g"] = s["g"] * 0.02                            # the first range's state reaches the last one
+    tol = 3 * ref.delta_tolerance(N)                  # the maps' and the joins' roundings on top
+    for js in ([0, T - 1], [T // r + 3, T // 2], [-1, T - 40]):
+        s["state_out_idx"] = torch.tensor(js[:b], dtype=torch.int32, device="cuda")
+        want = check(s, dtype, l2=True, tol=tol)
+    held = s["init_state"].clone() if init else None
+    got = ssd.ssd_gated_delta_fwd(**dict(s, init_state=held), qk_l2norm=True, final_state=held)
+    torch.cuda.synchronize()
+    for a, c in zip(want, got):
+        assert torch.equal(a, c)
+
+
+def test_ranges_only_where_few_heads_leave_the_gpu_idle():
+    assert ranges_of(8, 2048, 32, 128, 128, 8, "bf16") == 1
+    assert ranges_of(1, 16384, 32, 128, 128, 8, "bf16") >= 4
+    assert ranges_of(1, 300, 1, 64, 64, 1, "bf16") == 1
+    assert ranges_of(2, 17, 1, 64, 64, 1, "f32") == 1
+
+
+def test_token_ranges_captured_and_on_two_streams():
+    s = inputs(23, 1, 1400, 2, 64, 64, 1, "bf16")
+    assert ranges_of(1, 1400, 2, 64, 64, 1, "bf16") >= 3
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = ssd.ssd_gated_delta_fwd(**s, qk_l2norm=True)
+    again = [ssd.ssd_gated_delta_fwd(**s, qk_l2norm=True) for _ in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = ssd.ssd_gated_delta_fwd(**s, qk_l2norm=True)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, c, d, e in zip(want, out, *again):
+            assert torch.equal(a, c) and torch.equal(a, d) and torch.equal(a, e)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [9, 150])
 def test_scale(T, dtype):
