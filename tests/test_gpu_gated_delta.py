@@ -58,6 +58,12 @@ def near(name, got, want, tol, dtype="f32"):
     assert worst <= 8 * tol, name
 
 
+def y_tolerance(N, dtype):
+    """The outputs of bf16 calls read the state and the chunk's own part in 16
+    bits of fraction (two bf16 each): 2^-15 of their terms."""
+    return ref.delta_tolerance(N) + (2.0 ** -13 if dtype == "bf16" else 0.0)
+
+
 def check(s, dtype, scale=None, l2=False, tol=None, **kw):
     N = s["q"].shape[3]
     y, fin, at = ssd.ssd_gated_delta_fwd(**s, scale=scale, qk_l2norm=l2, **kw)
@@ -71,9 +77,7 @@ def check(s, dtype, scale=None, l2=False, tol=None, **kw):
             if j < 0:
                 held = s["init_state"]
                 assert torch.equal(at[i], torch.zeros_like(at[i]) if held is None else held[i])
-    # The outputs of bf16 calls read the state and the chunk's own part in 16
-    # bits of fraction (two bf16 each): 2^-15 of their terms.
-    near("y", y, wy, tol if dtype == "f32" else tol + 2.0 ** -13, dtype)
+    near("y", y, wy, y_tolerance(N, dtype) + tol - ref.delta_tolerance(N), dtype)
     return y, fin, at
 
 
@@ -253,6 +257,65 @@ def test_growth_is_computed_as_given(T):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e-30, 1e-12, 1e-5, 1e5, 1e12, 1e30])
+def test_values_of_any_size(size, dtype):
+    s = inputs(24, 2, 100, 2, 32, 64, 1, dtype, unit=True)
+    s["v"], s["init_state"] = (s["v"].float() * size).to(s["v"].dtype), s["init_state"] * size
+    check(s, dtype)
+    s["init_state"] = None
+    check(s, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e-15, 1e-4, 1e4, 1e15])
+def test_keys_and_queries_of_any_size(size, dtype):
+    # The rule with keys s k, beta / s^2 and values v is that of keys k, beta and
+    # values v / s (and the state times 1 / s); queries are scaled back.
+    s = inputs(25, 2, 100, 2, 32, 64, 1, dtype, init=False, unit=True)
+    s["k"], s["q"] = ((s[n].float() * f).to(s[n].dtype) for n, f in (("k", size), ("q", 1 / size)))
+    s["beta"] = s["beta"] / size ** 2
+    check(s, dtype)
+    check(dict(s, beta=s["beta"] * size ** 2), dtype, l2=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [200, 1100])
+def test_sizes_that_change_along_the_sequence(T, dtype):
+    # Values grow and shrink by 1e7 from one part to the next while strong decays
+    # let the state follow; columns of the values differ as much, so each is
+    # held to its own size.
+    s = inputs(26, 2, T, 2, 32, 64, 1, dtype, unit=True)
+    f = torch.ones(T)
+    f[T // 3:] = 1e7
+    f[T // 2:] = 1e-6
+    s["v"] = (s["v"].float() * f.cuda()[None, :, None, None]).to(s["v"].dtype)
+    s["g"] = s["g"].clone()
+    s["g"][:, [T // 3, T // 2]] = -80.0
+    y, fin, at = ssd.ssd_gated_delta_fwd(**s)
+    torch.cuda.synchronize()
+    wy, wf, wa = want_of(s)
+    tol = 3 * ref.delta_tolerance(64)
+    near("final_state", fin, wf, tol)
+    for i in range(2):
+        near("state_out", at[i], wa[i], tol)
+    for a, e in ((0, T // 3), (T // 3, T // 2), (T // 2, T)):
+        near("y", y[:, a:e], wy[:, a:e], 3 * y_tolerance(64, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_columns_of_different_sizes(dtype):
+    s = inputs(27, 2, 150, 2, 64, 64, 1, dtype, unit=True)
+    f = torch.logspace(-3, 3, 64).cuda()
+    s["v"], s["init_state"] = (s["v"].float() * f).to(s["v"].dtype), s["init_state"] * f[:, None]
+    y, fin, _ = ssd.ssd_gated_delta_fwd(**s)
+    torch.cuda.synchronize()
+    wy, wf, _ = want_of(s)
+    for c in range(0, 64, 7):
+        near(f"column {c}", fin[:, :, c], wf[:, :, c], ref.delta_tolerance(64))
+        near(f"column {c}", y[..., c], wy[..., c], y_tolerance(64, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [5, 100])
 def test_zero_beta_and_zero_keys(T, dtype):
     s = inputs(7, 2, T, 2, 32, 64, 1, dtype, unit=True)
@@ -308,7 +371,7 @@ def test_two_calls_continue_one(cut, dtype):
     wy, wf, _ = want_of(s, l2=True)
     tol = ref.delta_tolerance(64)
     near("final_state", fin, wf, 2 * tol)
-    near("y", torch.cat([y0, y1], 1), wy, 2 * tol + (2.0 ** -13 if dtype == "bf16" else 0.0), dtype)
+    near("y", torch.cat([y0, y1], 1), wy, tol + y_tolerance(64, dtype), dtype)
 
 
 @pytest.mark.parametrize("T", [3, 70])
@@ -442,7 +505,7 @@ def test_padded_batch_takes_each_sequences_state():
         one = {k: t[i:i + 1, :n] for k, t in s.items() if k not in ("init_state", "state_out_idx")}
         wy, wf, _ = want_of(dict(one, init_state=s["init_state"][i:i + 1], state_out_idx=None), l2=True)
         near("state", at[i:i + 1], wf, tol)
-        near("y", y[i:i + 1, :n], wy, tol + 2.0 ** -13, "bf16")
+        near("y", y[i:i + 1, :n], wy, y_tolerance(64, "bf16"), "bf16")
 
 
 def test_large_offsets():
