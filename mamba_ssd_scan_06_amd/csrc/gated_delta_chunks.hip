@@ -889,33 +889,44 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 // init_state aside, which the last range may overwrite (in-place calls) before
 // the first one starts.
 constexpr int kJoinRow = 256 + 4;
-__global__ __launch_bounds__(1024) void delta_join(DeltaParams p) {
+template <int NT>  // N / 16
+__global__ __launch_bounds__(64 * NT) void delta_join(DeltaParams p) {
     __shared__ __attribute__((aligned(16))) float held[16][kJoinRow];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, g = lane >> 4, N = p.dstate;
-    const unsigned tiles = (unsigned)p.headdim / 16, bh = blockIdx.x / tiles, tile = blockIdx.x - bh * tiles;
-    const int64_t BH = p.batch * p.nheads, v_state = (int64_t)p.headdim * N, mine = bh * v_state + (int64_t)tile * 16 * N;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i16 = lane & 15, g = lane >> 4;
+    constexpr int N = 16 * NT;
+    // Tiles of a head lie nheads apart, so they share an L2 where that is a multiple of 8.
+    const unsigned heads = (unsigned)(p.batch * p.nheads), tile = blockIdx.x / heads, bh = blockIdx.x - tile * heads;
+    const int64_t BH = heads, v_state = (int64_t)p.headdim * N, mine = bh * v_state + (int64_t)tile * 16 * N;
     if (p.init_state)
         for (int i = 4 * tid; i < 16 * N; i += 4 * (int)blockDim.x)
             *reinterpret_cast<f32x4 *>(p.range_init + mine + i) = *reinterpret_cast<const f32x4 *>(p.init_state + mine + i);
     for (int i = 4 * tid; i < 16 * N; i += 4 * (int)blockDim.x)
         *reinterpret_cast<f32x4 *>(&held[i / N][i % N]) = *reinterpret_cast<const f32x4 *>(p.range_state + mine + i);
-    __syncthreads();
     const int n = 16 * wave + i16;  // this lane's column, rows 4 g + r
+    f32x4 map[NT], acc;             // a range's map and state, read a range ahead
+    const unsigned at = 4 * g * N + n;
+    auto fetch = [&](int r) {
+        const float *m = p.range_map + ((int64_t)(r - 1) * BH + bh) * N * N;
+        const float *d = p.range_state + (int64_t)r * BH * v_state + mine;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) map[j][k] = (m + (16 * j + k) * N)[at];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = (d + k * N)[at];
+    };
+    if (p.ranges > 2) fetch(1);
+    __syncthreads();
     for (int r = 1; r + 1 < p.ranges; ++r) {
-        const float *m = p.range_map + ((int64_t)(r - 1) * BH + bh) * N * N + n;
-        float *d = p.range_state + (int64_t)r * BH * v_state + mine + n;
-        f32x4 acc;
+        f32x4 sum = acc;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[k] = d[(4 * g + k) * N];
-        for (int k0 = 0; k0 < N; k0 += 16) {
-            f32x4 b;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) b[k] = m[(int64_t)(k0 + 4 * g + k) * N];
-            acc = mma_f32_16(*reinterpret_cast<const f32x4 *>(&held[i16][k0 + 4 * g]), b, acc);
-        }
+        for (int j = 0; j < NT; ++j)
+            sum = mma_f32_16(*reinterpret_cast<const f32x4 *>(&held[i16][16 * j + 4 * g]), map[j], sum);
+        if (r + 2 < p.ranges) fetch(r + 1);
         __syncthreads();
+        float *d = p.range_state + (int64_t)r * BH * v_state + mine;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) held[4 * g + k][n] = d[(4 * g + k) * N] = acc[k];
+        for (int k = 0; k < 4; ++k) held[4 * g + k][n] = (d + k * N)[at] = sum[k];
         __syncthreads();
     }
 }
@@ -946,7 +957,9 @@ hipError_t launch(const DeltaParams &given, hipStream_t stream) {
                 <<<(unsigned)(heads * (p.ranges - 1) * (v_slices + n_slices)), kThreads, 0, stream>>>(p);
             hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
-            delta_join<<<(unsigned)(heads * (p.headdim / 16)), 64 * (p.dstate / 16), 0, stream>>>(p);
+            const unsigned tiles = (unsigned)(heads * (p.headdim / 16)), threads = 4 * p.dstate;
+            if (p.dstate % 32) delta_join<2 * NB - 1><<<tiles, threads, 0, stream>>>(p);
+            else delta_join<2 * NB><<<tiles, threads, 0, stream>>>(p);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         delta_chunks<T, NB, BUFS, WAVES, D, true><<<(unsigned)(heads * p.ranges * v_slices), kThreads, 0, stream>>>(p);
@@ -990,9 +1003,10 @@ hipError_t run(const DeltaParams &p, hipStream_t stream) {
 // to be filled; the first pass computes no outputs (0.8), and its workgroups are
 // more (the maps' rows); the launches and the join add about 5 + 0.6 per range.
 // Measured, 16384 tokens of 32 heads (N and P 128, bf16) in 1, 2, 3, 4, 6, 8 and
-// 10 ranges: 861, 791, 562, 501, 533, 505 and 575 us; 1021 tokens of 30 heads
-// (N 96, P 80, fp32: one workgroup per unit) in 1, 2, 3, 4 and 6: 105, 103, 87,
-// 99 and 133 us.
+// 10 ranges: 861, 791, 552, 485, 505, 471 and 518 us; 1021 tokens of 30 heads
+// (N 96, P 80, fp32: one workgroup per unit) in 1, 2, 3, 4 and 6: 103, 101, 79,
+// 86 and 109 us; 32768 tokens of 8 heads in 1, 4, 8 and 16: 1645, 789, 434 and
+// 295 us.
 void delta_ranges(DeltaParams &p, Elem e) {
     p.ranges = 1;
     p.range_chunks = p.nchunks;
