@@ -4,7 +4,7 @@
 //     S = e^g S;   r = v - S k;   S += beta r k';   y = scale S q
 //
 // Every row p of S [P,N] is on its own, so a workgroup takes 32 rows of one
-// (sequence, head) with 8 lanes per row and the row in their registers: the
+// (sequence, head), or 64, with 8 lanes per row and the row in their registers: the
 // state is read once and written once, 16 bytes per lane, and S k and S q are
 // joined over a row's lanes by three lane exchanges.  k, q (fp32, normalised
 // where asked), v, e^g and beta of 8 tokens at a time are laid out in LDS by the
@@ -15,7 +15,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kRows = 32;    // rows of a workgroup
+constexpr int kRows = 32;    // rows of a workgroup, of each of a lane's R
 constexpr int kLanes = 8;    // lanes of a row
 constexpr int kBlock = 8;    // tokens laid out at a time
 constexpr float kNormEps = 1e-6f;
@@ -34,33 +34,38 @@ __device__ __forceinline__ float sum8(float v) {
 
 // M: 16-byte pieces of a row per lane; piece m of lane l holds n = 4 (8 m + l)
 // and the three after it.
-template <typename T, int M>
+template <typename T, int M, int R>
 __global__ __launch_bounds__(kRows * kLanes) void delta_tokens(DeltaParams p) {
     constexpr int NP = M * kLanes * 4;  // N, rounded up to whole pieces of all lanes
     __shared__ __attribute__((aligned(16))) float ks[kBlock][NP], qs[kBlock][NP];
-    __shared__ float vs[kBlock][kRows], ys[kBlock][kRows], decay[kBlock], share[kBlock];
+    __shared__ float vs[kBlock][R * kRows], ys[kBlock][R * kRows], decay[kBlock], share[kBlock];
     const int tid = threadIdx.x, lane = tid & (kLanes - 1), row = tid / kLanes, wave = tid >> 6;
-    const int slices = (p.headdim + kRows - 1) / kRows;
+    const int slices = (p.headdim + R * kRows - 1) / (R * kRows);
     const unsigned item = blockIdx.x / (unsigned)slices, slice = blockIdx.x - item * (unsigned)slices;
     const unsigned b = item / (unsigned)p.nheads, h = item - b * (unsigned)p.nheads;
-    const int N = p.dstate, pieces = N / 4, p0 = (int)slice * kRows, rows = min(kRows, p.headdim - p0);
-    const bool live = row < rows;
-    const int64_t s_off = ((int64_t)item * p.headdim + p0 + min(row, rows - 1)) * N + 4 * lane;
+    const int N = p.dstate, pieces = N / 4, p0 = (int)slice * R * kRows, rows = min(R * kRows, p.headdim - p0);
+    const int64_t s_off = ((int64_t)item * p.headdim + p0 + row) * N + 4 * lane;  // of the first row
 
-    f32x4 s[M];
+    f32x4 s[R][M];
     auto store_state = [&](float *to) {
-        if (!live) return;
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-            if (kLanes * m + lane < pieces)
-                __builtin_nontemporal_store(s[m], reinterpret_cast<f32x4 *>(to + s_off + 4 * kLanes * m));
+        for (int r = 0; r < R; ++r)
+            if (row + r * kRows < rows)
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+                    if (kLanes * m + lane < pieces)
+                        __builtin_nontemporal_store(
+                            s[r][m], reinterpret_cast<f32x4 *>(to + s_off + (int64_t)r * kRows * N + 4 * kLanes * m));
     };
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-        s[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (p.init_state && kLanes * m + lane < pieces)
-            s[m] = __builtin_nontemporal_load(reinterpret_cast<const f32x4 *>(p.init_state + s_off + 4 * kLanes * m));
-    }
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            s[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (p.init_state && row + r * kRows < rows && kLanes * m + lane < pieces)
+                s[r][m] = __builtin_nontemporal_load(
+                    reinterpret_cast<const f32x4 *>(p.init_state + s_off + (int64_t)r * kRows * N + 4 * kLanes * m));
+        }
     int64_t at = -2;  // the accepted index
     if (p.state_out) {
         at = min(max((int64_t)p.state_out_idx[b], (int64_t)-1), p.seqlen - 1);
@@ -97,9 +102,11 @@ __global__ __launch_bounds__(kRows * kLanes) void delta_tokens(DeltaParams p) {
             }
         }
         {
-            const int t = tid / kRows, r = tid & (kRows - 1);  // kBlock x kRows values by as many threads
-            if (t < count && r < rows)
-                vs[t][r] = to_f32((reinterpret_cast<const T *>(p.v) + b * p.v_bs + (t0 + t) * p.v_ts)[(int64_t)h * p.headdim + p0 + r]);
+            const int t = tid / kRows;  // kBlock x kRows values by as many threads
+#pragma unroll
+            for (int r = tid & (kRows - 1); r < R * kRows; r += kRows)
+                if (t < count && r < rows)
+                    vs[t][r] = to_f32((reinterpret_cast<const T *>(p.v) + b * p.v_bs + (t0 + t) * p.v_ts)[(int64_t)h * p.headdim + p0 + r]);
             if (tid < count) {
                 decay[tid] = p.g ? expf(p.g[b * p.g_bs + (t0 + tid) * p.g_ts + h]) : 1.0f;
                 share[tid] = p.beta[b * p.beta_bs + (t0 + tid) * p.beta_ts + h];
@@ -108,38 +115,47 @@ __global__ __launch_bounds__(kRows * kLanes) void delta_tokens(DeltaParams p) {
         __syncthreads();
         for (int t = 0; t < count; ++t) {
             const float a = decay[t];
-            float dot = 0.0f;
+            float dot[R] = {}, out[R] = {}, u[R];
             f32x4 k[M];
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 k[m] = *reinterpret_cast<const f32x4 *>(&ks[t][4 * (kLanes * m + lane)]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[m][i] *= a;
-                    dot = fmaf(s[m][i], k[m][i], dot);
-                }
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[r][m][i] *= a;
+                        dot[r] = fmaf(s[r][m][i], k[m][i], dot[r]);
+                    }
             }
-            const float u = share[t] * (vs[t][row] - sum8(dot));
-            float out = 0.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) u[r] = share[t] * (vs[t][row + r * kRows] - sum8(dot[r]));
 #pragma unroll
             for (int m = 0; m < M; ++m) {
                 const f32x4 q = *reinterpret_cast<const f32x4 *>(&qs[t][4 * (kLanes * m + lane)]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s[m][i] = fmaf(u, k[m][i], s[m][i]);
-                    out = fmaf(s[m][i], q[i], out);
-                }
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[r][m][i] = fmaf(u[r], k[m][i], s[r][m][i]);
+                        out[r] = fmaf(s[r][m][i], q[i], out[r]);
+                    }
             }
-            out = sum8(out);
-            if (lane == 0) ys[t][row] = out;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                out[r] = sum8(out[r]);
+                if (lane == 0) ys[t][row + r * kRows] = out[r];
+            }
             if (t0 + t == at) store_state(p.state_out);
         }
         __syncthreads();
         {
-            const int t = tid / kRows, r = tid & (kRows - 1);
-            if (t < count && r < rows)
-                (reinterpret_cast<T *>(p.y) + ((int64_t)b * p.seqlen + t0 + t) * p.nheads * p.headdim)[(int64_t)h * p.headdim + p0 + r] =
-                    from_f32<T>(ys[t][r]);
+            const int t = tid / kRows;
+#pragma unroll
+            for (int r = tid & (kRows - 1); r < R * kRows; r += kRows)
+                if (t < count && r < rows)
+                    (reinterpret_cast<T *>(p.y) + ((int64_t)b * p.seqlen + t0 + t) * p.nheads * p.headdim)[(int64_t)h * p.headdim + p0 + r] =
+                        from_f32<T>(ys[t][r]);
         }
         // The next block's first barrier stands between these reads of ys and
         // its writes.
@@ -149,8 +165,22 @@ __global__ __launch_bounds__(kRows * kLanes) void delta_tokens(DeltaParams p) {
 
 template <typename T, int M>
 hipError_t launch(const DeltaParams &p, hipStream_t stream) {
-    const unsigned grid = (unsigned)(p.batch * p.nheads * ((p.headdim + kRows - 1) / kRows));
-    delta_tokens<T, M><<<grid, kRows * kLanes, 0, stream>>>(p);
+    // Two rows per lane halve the reads of k and q from LDS, where enough
+    // workgroups remain: N and P 128, 32 heads, 9 tokens of 8, 16 and 64 sequences
+    // 14.0, 27.3 and 101 us with one, 15.2, 21.9 and 90 with two.  N beyond 160 has
+    // too many registers (256, 16 heads, 16 tokens of 32 sequences: 129 and 142);
+    // for 2 tokens of 64 sequences only the states' traffic counts, which more waves
+    // carry better (70 and 75; 16 sequences 18.6 and 16.7).
+    const int64_t pairs = p.batch * p.nheads * ((p.headdim + 2 * kRows - 1) / (2 * kRows));
+    const bool two = M <= 5 && pairs >= 1024 && (p.seqlen >= 4 || pairs < 4096);
+    const int rows = two ? 2 * kRows : kRows;
+    const unsigned grid = (unsigned)(p.batch * p.nheads * ((p.headdim + rows - 1) / rows));
+    if constexpr (M <= 5)
+        if (two) {
+            delta_tokens<T, M, 2><<<grid, kRows * kLanes, 0, stream>>>(p);
+            return hipGetLastError();
+        }
+    delta_tokens<T, M, 1><<<grid, kRows * kLanes, 0, stream>>>(p);
     return hipGetLastError();
 }
 

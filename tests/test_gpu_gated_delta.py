@@ -123,6 +123,15 @@ def test_many_heads(N, dtype, lead):
     check(inputs(20, 9, 70, 32, 16, N, 8, dtype, lead=lead, unit=True), dtype)
 
 
+@pytest.mark.parametrize("T", [1, 3, 4, 9, 16])
+@pytest.mark.parametrize("P,N,dtype", [(16, 160, "bf16"), (48, 16, "f32"), (64, 64, "bf16"), (80, 96, "f32"),
+                                       (112, 128, "bf16"), (144, 48, "bf16"), (32, 176, "f32")])
+def test_many_heads_few_tokens(P, N, dtype, T):
+    # Enough rows for two per lane.
+    announce(P, N, dtype, T)
+    check(inputs(28, 18, T, 64, P, N, 8, dtype, pad=8), dtype, l2=True)
+
+
 @pytest.mark.parametrize("dtype,lead", [("bf16", 0), ("bf16", 3), ("f32", 0)])
 def test_many_heads_several_slices(dtype, lead):
     check(inputs(21, 5, 97, 32, 80, 128, 4, dtype, lead=lead), dtype, l2=True)
