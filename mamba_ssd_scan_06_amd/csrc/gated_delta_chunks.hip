@@ -384,22 +384,28 @@ template <typename T>
 __device__ __forceinline__ int v_swz(int r) {
     return sizeof(T) == 2 ? 2 * ((r >> 1) & 3) : 0;
 }
+template <typename T, int NB, bool OUT>
+struct Queries {
+    alignas(16) bf16 q[kIn<T>][C][32 * NB];
+};
 template <typename T, int NB>
-struct Buffer {
+struct Queries<T, NB, false> {};  // without outputs there is room for more workgroups
+template <typename T, int NB, bool OUT>
+struct Buffer : Queries<T, NB, OUT> {
     static constexpr int kPlane = 32 * NB;           // elements of a row of keys or queries
     static constexpr int kVRow = kSlice + (sizeof(T) == 2 ? 0 : 8);
     alignas(16) bf16 k[kIn<T>][C][kPlane];
-    alignas(16) bf16 q[kIn<T>][C][kPlane];
     alignas(16) T v[C][kVRow];
     alignas(16) char pack[Pack32<T>::kBytes];
 };
 
 // What a thread carries from global memory to LDS, one chunk ahead.
-template <typename T, int NB>
+template <typename T, int NB, bool OUT>
 struct Carry {
     static constexpr int VEC = 16 / sizeof(T), WORDS = 8 / VEC;  // 16-byte words of 8 elements
     static constexpr int kPackWords = (Pack32<T>::kBytes / 16 + kThreads - 1) / kThreads;
-    u32x4 kq[NB][WORDS], v[WORDS], pack[kPackWords];
+    static constexpr int kKeys = OUT ? NB : (NB + 1) / 2;
+    u32x4 kq[kKeys][WORDS], v[WORDS], pack[kPackWords];
 };
 
 // WAVES: waves per SIMD to leave registers for (two keep the accumulators in
@@ -413,8 +419,8 @@ struct Carry {
 template <typename T, int NB, int BUFS, int WAVES, bool DIRECT, bool OUT>
 __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     typedef Pack32<T> L;
-    typedef Buffer<T, NB> Buf;
-    typedef Carry<T, NB> Regs;
+    typedef Buffer<T, NB, OUT> Buf;
+    typedef Carry<T, NB, OUT> Regs;
     constexpr int NI = kIn<T>, NO = kOut<T>;
     static_assert(!DIRECT || (sizeof(T) == 2 && BUFS == 2 && L::kBytes == 8 * 1024), "direct copies");
     // Two objects, so that the compiler knows reads of one apart from the copies
@@ -461,12 +467,18 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     // cycles of a chunk).  Nothing branches: the last chunk's copies of a chunk
     // that is not there read an empty buffer.
     const int uwave = __builtin_amdgcn_readfirstlane(wave);
-    constexpr int kKeySteps = OUT ? NB : (NB + 1) / 2, kSteps = kKeySteps + 3;
-    uint32_t kq_off[NB], v_off;
+    constexpr int kKeySteps = Regs::kKeys, kSteps = kKeySteps + 3;
+    // A thread's or wave's piece of the keys (then queries) may be none.
+    auto none = [&](bool is_q) { return !OUT && is_q; };
+    auto keys_or_queries = [&](Buf &to, bool is_q, int e) __attribute__((always_inline)) {
+        if constexpr (OUT) return is_q ? &to.q[e][0][0] : &to.k[e][0][0];
+        else return &to.k[e][0][0];
+    };
+    uint32_t kq_off[kKeySteps], v_off;
     auto is_query = [&](int k) { return 4 * k + uwave >= 2 * NB; };
     if constexpr (DIRECT) {
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
+        for (int k = 0; k < kKeySteps; ++k) {
             const int at = 64 * (4 * k + uwave - (is_query(k) ? 2 * NB : 0)) + lane, row = at / (4 * NB);
             const int n = 8 * ((at % (4 * NB)) ^ key_swz<NB>(row));
             kq_off[k] = n < N ? 2u * ((uint32_t)row * (uint32_t)(is_query(k) ? p.q_ts : p.k_ts) + (uint32_t)n) : 0xffffff00u;
@@ -487,8 +499,9 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         auto bytes = [&](int64_t ts, int inner) { return left_next > 0 ? 2u * (before * (uint32_t)ts + (uint32_t)inner) : 0u; };
         if (k < kKeySteps) {
             const bool q = is_query(k);
+            if (none(q)) return;
             copy(q ? q_next : k_next, bytes(q ? p.q_ts : p.k_ts, N), kq_off[k],
-                 q ? &to.q[0][0][0] + 512 * (4 * k + uwave - 2 * NB) : &to.k[0][0][0] + 512 * (4 * k + uwave));
+                 keys_or_queries(to, q, 0) + 512 * (4 * k + uwave - (q ? 2 * NB : 0)));
         } else if (k == kKeySteps) {
             copy(v_next, map ? 0u : bytes(p.v_ts, v_cols), v_off, &to.v[0][0] + 512 * uwave);
         } else {
@@ -507,7 +520,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     // are 0), columns past N are 0.  A thread's pieces keep their rows and
     // columns, so their addresses only move on by a chunk; they are taken anew
     // for the last one, which may be cut short.
-    const T *kq_at[NB], *v_at;
+    const T *kq_at[kKeySteps], *v_at;
     const int v_row = tid >> 3, v_col = 8 * (tid & 7);
     auto piece_of = [&](int i, bool &is_q, int &row, int &n) {
         const int at = tid + kThreads * i;
@@ -519,7 +532,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     auto point = [&]() {  // at the next chunk
         const int left = min(left_next, C) - 1;  // the last row
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
+        for (int i = 0; i < kKeySteps; ++i) {
             bool is_q;
             int row, n;
             piece_of(i, is_q, row, n);
@@ -531,7 +544,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     auto fetch = [&](Regs &r, Buf &to) __attribute__((always_inline)) {
         if (left_next < C) point();
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
+        for (int i = 0; i < kKeySteps; ++i) {
 #pragma unroll
             for (int j = 0; j < Regs::WORDS; ++j) r.kq[i][j] = load_words(kq_at[i] + j * Regs::VEC);
             bool is_q;
@@ -558,14 +571,14 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     };
     auto place = [&](const Regs &r, Buf &to) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
+        for (int i = 0; i < kKeySteps; ++i) {
             bool is_q;
             int row, n;
             piece_of(i, is_q, row, n);
-            if (n >= N) continue;
-            const int sw = 8 * key_swz<NB>(row);
+            if (n >= N || none(is_q)) continue;
+            const int in_plane = row * Buf::kPlane + (n ^ 8 * key_swz<NB>(row));
             if constexpr (NI == 1) {
-                *reinterpret_cast<u32x4 *>(is_q ? &to.q[0][row][n ^ sw] : &to.k[0][row][n ^ sw]) = r.kq[i][0];
+                *reinterpret_cast<u32x4 *>(keys_or_queries(to, is_q, 0) + in_plane) = r.kq[i][0];
             } else {
                 float f[8];
 #pragma unroll
@@ -574,7 +587,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 split(f, t);
 #pragma unroll
                 for (int e = 0; e < NI; ++e)
-                    *reinterpret_cast<bf16x8 *>(is_q ? &to.q[e][row][n ^ sw] : &to.k[e][row][n ^ sw]) = t[e];
+                    *reinterpret_cast<bf16x8 *>(keys_or_queries(to, is_q, e) + in_plane) = t[e];
             }
         }
 #pragma unroll
@@ -660,6 +673,9 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     wait_vmcnt<0>();
     __syncthreads();
     char *y_at = reinterpret_cast<char *>(p.y) + ((int64_t)b * p.seqlen + first) * (int64_t)y_row;
+    bf16x4 minus_one;  // -1 times the identity
+#pragma unroll
+    for (int r = 0; r < 4; ++r) minus_one[r] = i16 == 4 * g + r ? (bf16)-1.0f : (bf16)0.0f;
     // The chunk whose first token is `t` from `buf`, while the next one comes into
     // `other`.
     auto chunk = [&](int t, const Buf &buf, Buf &other) __attribute__((always_inline)) {
@@ -691,26 +707,58 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             };
             // S k (rows: tokens); the terms of S are kept for S q (rows: p).
             f32x4 ks[2] = {};
-            bf16x8 sf[NB][NO], kf[2][2][NI], qf[2][2][NI];
+            // What a term leaves of S is a product of the matrix cores too: the state's
+            // tile minus the unit matrix times the term, exact, in the place of two
+            // vector instructions per value, which such a wave is bound by (16384 tokens
+            // of 32 heads in one range 861 -> 799 us).  Each step splits the next one's
+            // part, so that nothing waits for it; where the registers do not hold that,
+            // or a lone wave per SIMD would wait, it is subtracted.
+            constexpr bool AHEAD = WAVES == 2 && (NB <= 4 || DIRECT);
+            bf16x8 sf[NB][AHEAD ? 3 : NO], kf[2][2][NI], qf[2][2][NI];
+            auto split_state = [&](int kb) {
+                f32x4 left[2] = {s[kb][0], s[kb][1]};
+#pragma unroll
+                for (int e = 0; e < 3; ++e) {
+                    float f[8];
+                    bf16x8 t[1];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = left[i >> 2][i & 3];
+                    split(f, t);
+                    sf[kb][e] = t[0];
+                    if (e < 2)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            left[half] = mfma(minus_one, half ? bf16x4{t[0][4], t[0][5], t[0][6], t[0][7]}
+                                                              : bf16x4{t[0][0], t[0][1], t[0][2], t[0][3]}, left[half]);
+                }
+            };
             rows_of(buf.k, 0, kf[0]);
+            if constexpr (AHEAD) split_state(0);
 #pragma unroll
             for (int kb = 0; kb < NB; ++kb) {
                 if (kb + 1 < NB) rows_of(buf.k, kb + 1, kf[(kb + 1) & 1]);
-                else if (OUT) rows_of(buf.q, 0, qf[0]);
+                else if constexpr (OUT) rows_of(buf.q, 0, qf[0]);
                 if (kb < kKeySteps) fetch_some(kb, kb + 1);
                 __builtin_amdgcn_sched_barrier(0);
-                float f[8];
+                if constexpr (AHEAD) {
+                    if (kb + 1 < NB) split_state(kb + 1);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = s[kb][i >> 2][i & 3];
-                bf16x8 st[3];
-                split(f, st);
+                    for (int I = 0; I < 2; ++I) mma_terms<NI, 3>(kf[kb & 1][I], sf[kb], ks[I]);
+                } else {
+                    float f[8];
 #pragma unroll
-                for (int e = 0; e < NO; ++e) sf[kb][e] = st[e];
+                    for (int i = 0; i < 8; ++i) f[i] = s[kb][i >> 2][i & 3];
+                    bf16x8 st[3];
+                    split(f, st);
 #pragma unroll
-                for (int I = 0; I < 2; ++I) mma_terms<NI, 3>(kf[kb & 1][I], st, ks[I]);
+                    for (int e = 0; e < NO; ++e) sf[kb][e] = st[e];
+#pragma unroll
+                    for (int I = 0; I < 2; ++I) mma_terms<NI, 3>(kf[kb & 1][I], st, ks[I]);
+                }
             }
             auto s_q = [&](int kb) {
-                if (OUT && kb + 1 < NB) rows_of(buf.q, kb + 1, qf[(kb + 1) & 1]);
+                if constexpr (OUT)
+                    if (kb + 1 < NB) rows_of(buf.q, kb + 1, qf[(kb + 1) & 1]);
                 fetch_some(kKeySteps + (kb == 0 ? 0 : kb + 1), kb + 1 == NB ? kSteps : kKeySteps + kb + 2);
                 __builtin_amdgcn_sched_barrier(0);
                 if (OUT)
@@ -934,11 +982,21 @@ __global__ __launch_bounds__(64 * NT) void delta_join(DeltaParams p) {
     }
 }
 
+// The LDS buffers of a workgroup, and the waves per SIMD that LDS and the size of
+// the state leave.
+constexpr int kLds = 160 * 1024;
+template <typename T, int NB, bool OUT>
+constexpr int buffers() {
+    static_assert(sizeof(Buffer<T, NB, OUT>) <= kLds, "LDS");
+    return 2 * sizeof(Buffer<T, NB, OUT>) <= kLds ? 2 : 1;
+}
+template <typename T, int NB, bool OUT>
+constexpr int waves_per_simd() {
+    return 2 * buffers<T, NB, OUT>() * sizeof(Buffer<T, NB, OUT>) <= kLds && NB <= 5 ? 2 : 1;
+}
+
 template <typename T, int NB>
 hipError_t launch(const DeltaParams &given, hipStream_t stream) {
-    constexpr int kLds = 160 * 1024;
-    constexpr int BUFS = 2 * sizeof(Buffer<T, NB>) <= kLds ? 2 : 1;
-    static_assert(BUFS * sizeof(Buffer<T, NB>) <= kLds, "LDS");
     // As many heads per wave of the preparation as share their keys while that
     // leaves two waves per SIMD (their rows are loaded and multiplied once: 62 ->
     // 40 us for 512 chunks of 32 heads in 8 groups).
@@ -952,11 +1010,10 @@ hipError_t launch(const DeltaParams &given, hipStream_t stream) {
     if (r != hipSuccess) return r;
     const int64_t v_slices = (p.headdim + kSlice - 1) / kSlice, n_slices = (p.dstate + kSlice - 1) / kSlice;
     const int64_t heads = p.batch * p.nheads;
-    constexpr int WAVES = 2 * BUFS * sizeof(Buffer<T, NB>) <= kLds && NB <= 5 ? 2 : 1;
     auto passes = [&](auto direct) {
         constexpr bool D = decltype(direct)::value;
         if (p.ranges > 1) {
-            delta_chunks<T, NB, BUFS, WAVES, D, false>
+            delta_chunks<T, NB, buffers<T, NB, false>(), waves_per_simd<T, NB, false>(), D, false>
                 <<<(unsigned)(heads * (p.ranges - 1) * (v_slices + n_slices)), kThreads, 0, stream>>>(p);
             hipError_t e = hipGetLastError();
             if (e != hipSuccess) return e;
@@ -965,7 +1022,8 @@ hipError_t launch(const DeltaParams &given, hipStream_t stream) {
             else delta_join<2 * NB><<<tiles, threads, 0, stream>>>(p);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        delta_chunks<T, NB, BUFS, WAVES, D, true><<<(unsigned)(heads * p.ranges * v_slices), kThreads, 0, stream>>>(p);
+        delta_chunks<T, NB, buffers<T, NB, true>(), waves_per_simd<T, NB, true>(), D, true>
+            <<<(unsigned)(heads * p.ranges * v_slices), kThreads, 0, stream>>>(p);
         return hipGetLastError();
     };
     if constexpr (sizeof(T) == 2) {
