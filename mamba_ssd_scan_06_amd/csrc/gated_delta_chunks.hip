@@ -1060,31 +1060,34 @@ hipError_t run(const DeltaParams &p, hipStream_t stream) {
 // the other, so a long sequence is cut into ranges of chunks that run side by
 // side, twice (see delta_chunks), with a join between.  In units of a chunk's
 // time with one workgroup per compute unit, a pass over ranges of L chunks takes
-// L, 1.75 L where two workgroups share a unit, and as often that as the GPU has
-// to be filled; the first pass computes no outputs (0.8), and its workgroups are
-// more (the maps' rows); the launches and the join add about 5 + 0.6 per range.
-// Measured, 16384 tokens of 32 heads (N and P 128, bf16) in 1, 2, 3, 4, 6, 8 and
-// 10 ranges: 861, 791, 552, 485, 505, 471 and 518 us; 1021 tokens of 30 heads
-// (N 96, P 80, fp32: one workgroup per unit) in 1, 2, 3, 4 and 6: 103, 101, 79,
-// 86 and 109 us; 32768 tokens of 8 heads in 1, 4, 8 and 16: 1645, 789, 434 and
-// 295 us.
+// L, (1 + 3 k) / 4 L where k workgroups share a unit, and as often that as the GPU has
+// to be filled; the first pass computes no outputs (0.65), and its workgroups are
+// more (the maps' rows); the launches and the join add about 2 + r.  Measured,
+// 16384 tokens of 32 heads (N and P 128, bf16) in 1, 2, 3, 4, 5, 7, 8, 10 and 16
+// ranges: 799, 751, 525, 472, 486, 455, 461, 498 and 491 us; 1021 tokens of 30
+// heads (N 96, P 80, fp32) in 1, 2, 3, 4, 5 and 6: 105, 97, 77, 71, 89 and 93 us;
+// 32768 tokens of 8 heads in 1, 4, 8 and 16: 1535, 746, 411 and 293 us; 2 x 4096
+// tokens of 32 heads in 1, 2, 3 and 4: 215, 207, 212 and 210 us.
 void delta_ranges(DeltaParams &p, Elem e) {
     p.ranges = 1;
     p.range_chunks = p.nchunks;
     if (p.nchunks < 2) return;
     const double heads = (double)p.batch * p.nheads;
     const int v_slices = (p.headdim + kSlice - 1) / kSlice, n_slices = (p.dstate + kSlice - 1) / kSlice;
-    const bool pairs = e == Elem::BF16 && p.dstate <= 160;  // two workgroups fit a compute unit
-    auto rounds = [&](double wgs) {
-        if (wgs <= 256.0) return 1.0;
-        return pairs ? 1.75 * ceil(wgs / 512.0) : ceil(wgs / 256.0);
+    // Workgroups that fit a compute unit (LDS and registers) in either pass.
+    const bool bf = e == Elem::BF16;
+    const double fit_first = bf ? (p.dstate <= 160 ? 4 : 2) : p.dstate <= 96 ? 2 : 1;
+    const double fit_second = p.dstate <= (bf ? 160 : 32) ? 2 : 1;
+    auto rounds = [](double wgs, double fit) {
+        const double each = ceil(wgs / 256.0), whole = floor(each / fit), rest = each - whole * fit;
+        return whole * (0.25 + 0.75 * fit) + (rest > 0.0 ? 0.25 + 0.75 * rest : 0.0);
     };
-    double best = 0.9 * (double)p.nchunks * rounds(heads * v_slices);
+    double best = 0.9 * (double)p.nchunks * rounds(heads * v_slices, fit_second);
     for (int r = 2; r <= 16; ++r) {
         const int64_t len = (p.nchunks + r - 1) / r;
         if ((p.nchunks + len - 1) / len != r) continue;  // fewer ranges of this length
         const double first = heads * (v_slices + (r - 2) * (v_slices + n_slices)), second = heads * v_slices * r;
-        const double cost = (double)len * (0.8 * rounds(first) + rounds(second)) + 5.0 + 0.6 * r;
+        const double cost = (double)len * (0.65 * rounds(first, fit_first) + rounds(second, fit_second)) + 2.0 + r;
         if (cost < best) {
             best = cost;
             p.ranges = r;
