@@ -692,6 +692,40 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
         f32x4 qs[2] = {};  // S q, then y
         if (live) {
             const float *tab = reinterpret_cast<const float *>(buf.pack + L::kTab);
+            // What a term leaves of the state or of the updates is a product of the
+            // matrix cores too: the tile minus the unit matrix times the term, exact, in
+            // the place of two vector instructions per value, which such a wave is bound
+            // by (16384 tokens of 32 heads in one range 861 -> 799 us with the state's;
+            // 2 x 4096 tokens 207 -> 202 with the updates').  The state's terms are taken
+            // a step ahead, so that nothing waits for them; where the registers do not
+            // hold that, or a lone wave per SIMD would wait, they are subtracted.
+            constexpr bool AHEAD = WAVES == 2 && (NB <= 4 || DIRECT);
+            auto split_tiles = [&](const f32x4 (&v)[2], auto &to) __attribute__((always_inline)) {
+                constexpr int TERMS = sizeof(to) / sizeof(bf16x8);
+                f32x4 left[2] = {v[0], v[1]};
+#pragma unroll
+                for (int e = 0; e < TERMS; ++e) {
+                    float f[8];
+                    bf16x8 t[1];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = left[i >> 2][i & 3];
+                    split(f, t);
+                    to[e] = t[0];
+                    if (e + 1 < TERMS)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            left[half] = mfma(minus_one, half ? bf16x4{t[0][4], t[0][5], t[0][6], t[0][7]}
+                                                              : bf16x4{t[0][0], t[0][1], t[0][2], t[0][3]}, left[half]);
+                }
+            };
+            auto split_values = [&](const float (&v)[8], auto &to) __attribute__((always_inline)) {
+                if constexpr (AHEAD) {
+                    const f32x4 tiles[2] = {{v[0], v[1], v[2], v[3]}, {v[4], v[5], v[6], v[7]}};
+                    split_tiles(tiles, to);
+                } else {
+                    split(v, to);
+                }
+            };
             // The order of what follows is written out, since with two waves per
             // SIMD at most a read of LDS right before its use costs its latency:
             // every operand is read one step ahead (a scheduling barrier keeps
@@ -707,31 +741,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             };
             // S k (rows: tokens); the terms of S are kept for S q (rows: p).
             f32x4 ks[2] = {};
-            // What a term leaves of S is a product of the matrix cores too: the state's
-            // tile minus the unit matrix times the term, exact, in the place of two
-            // vector instructions per value, which such a wave is bound by (16384 tokens
-            // of 32 heads in one range 861 -> 799 us).  Each step splits the next one's
-            // part, so that nothing waits for it; where the registers do not hold that,
-            // or a lone wave per SIMD would wait, it is subtracted.
-            constexpr bool AHEAD = WAVES == 2 && (NB <= 4 || DIRECT);
             bf16x8 sf[NB][AHEAD ? 3 : NO], kf[2][2][NI], qf[2][2][NI];
-            auto split_state = [&](int kb) {
-                f32x4 left[2] = {s[kb][0], s[kb][1]};
-#pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    float f[8];
-                    bf16x8 t[1];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = left[i >> 2][i & 3];
-                    split(f, t);
-                    sf[kb][e] = t[0];
-                    if (e < 2)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            left[half] = mfma(minus_one, half ? bf16x4{t[0][4], t[0][5], t[0][6], t[0][7]}
-                                                              : bf16x4{t[0][0], t[0][1], t[0][2], t[0][3]}, left[half]);
-                }
-            };
+            auto split_state = [&](int kb) { split_tiles(s[kb], sf[kb]); };
             rows_of(buf.k, 0, kf[0]);
             if constexpr (AHEAD) split_state(0);
 #pragma unroll
@@ -794,7 +805,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             }
             if (NB > 1) s_q(1);
             else __builtin_amdgcn_sched_barrier(0);
-            split(x, xf);
+            split(x, xf);  // the chain waits for this one
 #pragma unroll
             for (int e = 0; e < 3; ++e) x0[e] = bf16x4{xf[e][0], xf[e][1], xf[e][2], xf[e][3]};
             f32x4 u[2] = {}, dv[2];
@@ -824,7 +835,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3] * wt[16 * (i >> 2) + 4 * g + (i & 3)];
                 bf16x8 uf[3];
-                split(uv, uf);
+                split_values(uv, uf);
                 f32x4 m[NB][2];
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb)
@@ -848,7 +859,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3] * dv[i >> 2][i & 3];
                 bf16x8 uf[3];
-                split(uv, uf);
+                split_values(uv, uf);
 #pragma unroll
                 for (int kb = 0; kb < NB; ++kb) {
                     bf16x8 next[2][NI];
@@ -877,7 +888,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3];
                 bf16x8 uf[NO];
                 bf16x4 u0[NO];
-                split(uv, uf);
+                split_values(uv, uf);
 #pragma unroll
                 for (int e = 0; e < NO; ++e) u0[e] = bf16x4{uf[e][0], uf[e][1], uf[e][2], uf[e][3]};
 #pragma unroll
