@@ -22,16 +22,19 @@ struct RowGrid {
     int lanes;  // threads per row, a power of two; a workgroup has max(lanes, 64)
 };
 
-// Sum over a row's lanes (all of the workgroup where lanes > 64).
-__device__ __forceinline__ float row_sum(float v, int lanes, float *waves) {
+// Sum over a row's lanes (all of the workgroup where lanes > 64).  Calls take the
+// two halves of `waves` in turn, so that the barrier of the one between stands
+// between a half's reads and its next writes.
+__device__ __forceinline__ float row_sum(float v, int lanes, float (&waves)[2][16], int &turn) {
     for (int m = 1; m < (lanes < 64 ? lanes : 64); m <<= 1) v += __shfl_xor(v, m);
     if (lanes > 64) {
         const int nw = lanes >> 6;
-        if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = v;
+        float *sums = waves[turn];
+        turn ^= 1;
+        if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = v;
         __syncthreads();
         v = 0.0f;
-        for (int w = 0; w < nw; ++w) v += waves[w];
-        __syncthreads();  // the next sum may write waves again
+        for (int w = 0; w < nw; ++w) v += sums[w];
     }
     return v;
 }
@@ -104,7 +107,8 @@ template <typename T, typename R, int HELD, int MAX>
 __global__ __launch_bounds__(MAX) void residual_norm_kernel(ResidualNormParams p, RowGrid gr) {
     constexpr int VEC = 16 / sizeof(T);
     typedef StreamPiece<T, R> Stream;
-    __shared__ float waves[16];
+    __shared__ float waves[2][16];
+    int turn = 0;
     const int lanes = gr.lanes, lane = threadIdx.x & (lanes - 1);
     const int per_wg = blockDim.x / lanes;
     // All threads of a workgroup take the same number of turns (barriers in
@@ -120,7 +124,7 @@ __global__ __launch_bounds__(MAX) void residual_norm_kernel(ResidualNormParams p
         T *out = reinterpret_cast<T *>(p.out) + (int64_t)row * p.dim;
         R *hout = p.residual_out ? reinterpret_cast<R *>(p.residual_out) + (int64_t)row * p.dim : nullptr;
 
-        auto scale_of = [&](float sum) { return 1.0f / sqrtf(row_sum(sum, lanes, waves) / (float)p.dim + p.eps); };
+        auto scale_of = [&](float sum) { return 1.0f / sqrtf(row_sum(sum, lanes, waves, turn) / (float)p.dim + p.eps); };
         // x -> h in place; n_scale is the first norm's factor (1 without it).
         auto stream_value = [&](float x_, float gate_, float post, float layer, float r_, float n_scale) {
             float v = x_ * n_scale;
@@ -147,6 +151,13 @@ __global__ __launch_bounds__(MAX) void residual_norm_kernel(ResidualNormParams p
                 if (gate) gt[m] = load_words(gate + at[m]);
                 if (res) rs[m].load(res + at[m]);
             }
+            // Few rows wait for every load in turn, so the vectors over the
+            // channels are loaded here too where a thread holds one piece.
+            constexpr bool EARLY = HELD == 1;
+            Channels<VEC> post = {}, layer = {}, w = {};
+            if (EARLY && p.post_weight) post.load(p.post_weight + at[0]);
+            if (EARLY && p.layer_scale) layer.load(p.layer_scale + at[0]);
+            if (EARLY && p.weight) w.load(p.weight + at[0]);
             auto sum_of = [&](int m, const float (&v)[VEC], float sum) {
                 const int shared = (m * lanes + lane) * VEC - at[m];  // all of them: no piece of its own
 #pragma unroll
@@ -168,9 +179,8 @@ __global__ __launch_bounds__(MAX) void residual_norm_kernel(ResidualNormParams p
             float v[HELD][VEC], sum = 0.0f;
 #pragma unroll
             for (int m = 0; m < HELD; ++m) {
-                Channels<VEC> post = {}, layer = {};
-                if (p.post_weight) post.load(p.post_weight + at[m]);
-                if (p.layer_scale) layer.load(p.layer_scale + at[m]);
+                if (!EARLY && p.post_weight) post.load(p.post_weight + at[m]);
+                if (!EARLY && p.layer_scale) layer.load(p.layer_scale + at[m]);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i)
                     v[m][i] = stream_value(word_f32(xr[m], i, T()), word_f32(gt[m], i, T()), post.get(i), layer.get(i),
@@ -186,8 +196,7 @@ __global__ __launch_bounds__(MAX) void residual_norm_kernel(ResidualNormParams p
                     hs.set(v[m]);
                     hs.store(hout + at[m]);
                 }
-                Channels<VEC> w = {};
-                if (p.weight) w.load(p.weight + at[m]);
+                if (!EARLY && p.weight) w.load(p.weight + at[m]);
                 float o[VEC];
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) o[i] = p.weight ? v[m][i] * scale * w.get(i) : v[m][i] * scale;
