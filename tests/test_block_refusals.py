@@ -137,17 +137,29 @@ def test_pairs_of_arguments():
 def test_workspace():
     c = Delta(b=1, T=500)
     need = ssd.ssd_gated_delta_workspace_bytes(c.shape, BF16)
+    assert need > 0
     assert ssd.ssd_gated_delta_workspace_bytes(Delta(T=1).shape, BF16) == 0
     assert ssd.ssd_gated_delta_workspace_bytes(Delta(N=24).shape, BF16) == 0 and ssd.ssd_last_error()
-    if need:
-        c.scalars["ws_bytes"] = need - 1
-        assert c() == ERR_WORKSPACE
-        c.scalars["ws_bytes"] = need
-        c.p["ws"] = None
-        assert c() == ERR_WORKSPACE
-        for k in ("y", "final", "at", "q", "k", "v", "init", "g", "beta"):
-            c.p["ws"] = c.p[k]
-            assert c() == ERR_ALIAS, k
+    c.scalars["ws_bytes"] = need - 1
+    assert c() == ERR_WORKSPACE
+    c.scalars["ws_bytes"] = need
+    c.p["ws"] = None
+    assert c() == ERR_WORKSPACE
+    for k in ("y", "final", "at", "q", "k", "v", "init", "g", "beta"):
+        c.p["ws"] = c.p[k]
+        assert c() == ERR_ALIAS, k
+    c.p["ws"] = Delta().p["ws"] + 8
+    assert c() == ERR_ALIGN
+
+
+def test_chunks_of_all_heads_are_bounded():
+    # The preparation numbers them in 32 bits.
+    for T, status in (((1 << 25) - 32, OK), ((1 << 25), ERR_UNSUPPORTED)):
+        c = Delta(b=1, T=T, H=64, P=16, N=16, G=1)
+        need = ssd.ssd_gated_delta_workspace_bytes(c.shape, BF16)
+        assert (need > 0) == (status == OK)
+        if status != OK:
+            assert c() == status
 
 
 def test_nothing_to_do():
