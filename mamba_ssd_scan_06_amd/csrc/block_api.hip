@@ -16,8 +16,11 @@ using ssd::product;
 using ssd::Range;
 using ssd::range;
 
-// Calls of more tokens run in chunks.
-constexpr int64_t kDeltaTokens = 16;
+// Calls of more tokens run in chunks.  N and P 128, 32 heads, token by token and in
+// chunks: bf16, 16 tokens of 1 and 64 sequences 14.3 / 14.2 and 117 / 114 us, 24
+// tokens 19.5 / 14.4 and 151 / 116; fp32, whose chunks cost twice as much, 24 tokens
+// 18.1 / 20.7 and 148 / 214, 32 tokens 22.7 / 20.9 and 182 / 221.
+int64_t delta_tokens(ssd_dtype dtype) { return dtype == SSD_DTYPE_BF16 ? 16 : 24; }
 
 ssd_status check_delta(const ssd_delta_shape *s, ssd_dtype dtype) {
     if (!s) return fail(SSD_ERR_NULL, "shape is NULL");
@@ -61,7 +64,7 @@ ssd::DeltaParams delta_params(const ssd_delta_shape *s, ssd_dtype dtype) {
     p.g_ts = used_stride(s->seqlen, s->g_token_stride);
     p.beta_bs = used_stride(s->batch, s->beta_batch_stride);
     p.beta_ts = used_stride(s->seqlen, s->beta_token_stride);
-    p.nchunks = s->seqlen > kDeltaTokens ? (s->seqlen + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk : 0;
+    p.nchunks = s->seqlen > delta_tokens(dtype) ? (s->seqlen + ssd::kDeltaChunk - 1) / ssd::kDeltaChunk : 0;
     ssd::delta_ranges(p, elem(dtype));
     return p;
 }

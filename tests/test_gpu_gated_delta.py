@@ -92,6 +92,9 @@ CASES = [
     (2, 8, 2, 256, 256, 2, "f32", True, True, True, 0, 0, True),
     (2, 16, 2, 48, 80, 1, "bf16", True, False, True, 5, 0, True),
     (5, 17, 2, 64, 128, 1, "f32", True, True, True, 0, 0, True),
+    (3, 24, 2, 128, 128, 1, "f32", True, True, True, 0, 0, True),
+    (3, 25, 2, 128, 128, 1, "f32", True, True, True, 0, 0, True),
+    (3, 17, 2, 128, 128, 1, "bf16", True, True, True, 0, 0, True),
     (2, 31, 2, 32, 32, 1, "bf16", True, True, True, 0, 0, True),
     (2, 32, 3, 16, 64, 3, "bf16", True, True, True, 0, 0, True),
     (5, 33, 4, 48, 16, 2, "bf16", True, True, True, 1, 0, True),
