@@ -193,7 +193,7 @@ def test_ranges_only_where_few_heads_leave_the_gpu_idle():
     assert ranges_of(8, 2048, 32, 128, 128, 8, "bf16") == 1
     assert ranges_of(1, 16384, 32, 128, 128, 8, "bf16") >= 4
     assert ranges_of(1, 300, 1, 64, 64, 1, "bf16") == 1
-    assert ranges_of(2, 17, 1, 64, 64, 1, "f32") == 1
+    assert ranges_of(2, 25, 1, 64, 64, 1, "f32") == 1
 
 
 def test_token_ranges_captured_and_on_two_streams():
