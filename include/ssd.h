@@ -537,9 +537,9 @@ typedef struct {
  *                                   non-NULL exactly when state_out_idx is
  *   workspace     16-byte aligned, ssd_gated_delta_workspace_bytes(...) bytes,
  *                 contents on entry ignored; may be NULL when that is 0
- * States are fp32 throughout and 16-byte aligned.  Values are finite; g and beta
- * need not be bounded, but keys of norm above sqrt(2 / beta) make the rule
- * itself grow.  A few tokens run token by token, prompts in chunks (this needs
+ * States are fp32 throughout and 16-byte aligned.  Values are finite, those of
+ * padding tokens too (products over whole chunks read them); g and beta need not
+ * be bounded, but keys of norm above sqrt(2 / beta) make the rule itself grow.  A few tokens run token by token, prompts in chunks (this needs
  * the workspace); the choice depends on the sizes and dtype alone.  With a
  * padded batch, j_b = length - 1 gives each sequence's own state.
  * batch, nheads <= 65535, T < 2^31, batch * nheads * ceil(P / 32) < 2^24,
