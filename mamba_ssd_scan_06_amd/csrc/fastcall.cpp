@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
 #include <torch/csrc/Exceptions.h>
@@ -67,6 +68,12 @@ int code_of(const Arg &a) {
     if (!a.ok || !a.t.defined() || !a.t.is_cuda()) return -1;
     if (a.t.device() != c10::impl::VirtualGuardImpl(at::kCUDA).getDevice()) return -1;
     return a.t.scalar_type() == at::kBFloat16 ? SSD_DTYPE_BF16 : a.t.scalar_type() == at::kFloat ? SSD_DTYPE_F32 : -1;
+}
+
+// A new dense tensor on the GPU: what at::empty makes behind the dispatcher, which
+// costs as much host time again.
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, at::Device dev) {
+    return at::Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
 }
 
 PyObject *none() { Py_RETURN_NONE; }
@@ -324,10 +331,10 @@ PyObject *delta(PyObject *, PyObject *const *a, Py_ssize_t n) {
             ssd_delta_shape s = {b,        T,        H,        P,        N,        G,        st(q, 0),    st(q, 1),
                                  st(k, 0), st(k, 1), st(v, 0), st(v, 1), st(g, 0), st(g, 1), st(beta, 0), st(beta, 1)};
             const size_t bytes = g_delta_bytes(&s, (ssd_dtype)code);
-            y = at::empty({b, T, H, P}, v.t.options());
-            if (!fin.t.defined() && want_final) fin.t = at::empty({b, H, P, N}, beta.t.options());
-            if (idx.t.defined()) at_j = at::empty({b, H, P, N}, beta.t.options());
-            if (bytes > 0) ws = at::empty({(int64_t)bytes}, beta.t.options().dtype(at::kByte));
+            y = fresh({b, T, H, P}, type, dev);
+            if (!fin.t.defined() && want_final) fin.t = fresh({b, H, P, N}, at::kFloat, dev);
+            if (idx.t.defined()) at_j = fresh({b, H, P, N}, at::kFloat, dev);
+            if (bytes > 0) ws = fresh({(int64_t)bytes}, at::kByte, dev);
             auto p = [](const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; };
             r = g_delta(q.ptr(), k.ptr(), v.ptr(), (const float *)g.ptr(), (const float *)beta.ptr(), scale, l2,
                         (const float *)init.ptr(), y.data_ptr(), (float *)fin.ptr(), (const int32_t *)idx.ptr(),
@@ -375,8 +382,8 @@ PyObject *residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         ssd_status st;
         {
             const Unlocked unlocked;
-            out = at::empty(x.t.sizes(), x.t.options());
-            h = at::empty(x.t.sizes(), x.t.options().dtype(type));
+            out = fresh(x.t.sizes(), x.t.scalar_type(), dev);
+            h = fresh(x.t.sizes(), type, dev);
             auto bs = [&](const Arg &t) { return !t.t.defined() || two ? 0 : t.t.stride(0); };
             auto ts = [&](const Arg &t) { return t.t.defined() ? t.t.stride(-2) : 0; };
             ssd_residual_norm_shape s = {b, T, dim, bs(x), ts(x), bs(res), ts(res), bs(gate), ts(gate)};
