@@ -315,13 +315,15 @@ hipError_t run(const ResidualNormParams &p, hipStream_t stream) {
     constexpr int VEC = 16 / sizeof(T);
     const int pieces = (p.dim + VEC - 1) / VEC;
     // The fewest lanes (at least 8) with three pieces each or fewer, and more while
-    // that leaves less than four waves per compute unit.  Four pieces leave too few
+    // that leaves less than eight waves per compute unit (256 rows of 4096 7.4 us with
+    // less than four, 6.2 with eight; sixteen splits 300 fp32 rows of 5120 once more:
+    // 8.7 and 12 us).  Four pieces leave too few
     // waves for the loads: 16384 rows of 4096 with everything 150 us with four, 136
     // with two of twice the lanes; three in the place of two of twice the lanes, of
     // which the last are partly idle: rows of 5120 179 and 205 us.
     RowGrid gr = {8};
     while (gr.lanes < 1024 && (pieces + gr.lanes - 1) / gr.lanes > 3) gr.lanes *= 2;
-    while (gr.lanes < 1024 && pieces > gr.lanes && p.rows * gr.lanes < 4 * 256 * 64) gr.lanes *= 2;
+    while (gr.lanes < 1024 && pieces > gr.lanes && p.rows * gr.lanes < 8 * 256 * 64) gr.lanes *= 2;
     const int each = (pieces + gr.lanes - 1) / gr.lanes;
     const int held = p.dim < VEC || each > kMaxHeld ? 0 : each;
     const int threads = std::max(gr.lanes, 64);
