@@ -1004,12 +1004,17 @@ __global__ __launch_bounds__(64 * NT) void delta_join(DeltaParams p) {
 }
 
 // The LDS buffers of a workgroup, and the waves per SIMD that LDS and the size of
-// the state leave.
+// the state leave.  One buffer where two workgroups fit a unit with one each but
+// not with two, and the registers hold what then passes through them: fp32, N 64
+// and 96, 64 and 32 heads of 8 x 1024 and 8 x 512 tokens 191 -> 170 and 118 -> 101
+// us (N 128, which spills: 137 -> 168).
 constexpr int kLds = 160 * 1024;
 template <typename T, int NB, bool OUT>
 constexpr int buffers() {
     static_assert(sizeof(Buffer<T, NB, OUT>) <= kLds, "LDS");
-    return 2 * sizeof(Buffer<T, NB, OUT>) <= kLds ? 2 : 1;
+    constexpr size_t bytes = sizeof(Buffer<T, NB, OUT>);
+    if (NB <= 3 && 2 * bytes <= kLds && 4 * bytes > kLds) return 1;
+    return 2 * bytes <= kLds ? 2 : 1;
 }
 template <typename T, int NB, bool OUT>
 constexpr int waves_per_simd() {
@@ -1098,7 +1103,7 @@ void delta_ranges(DeltaParams &p, Elem e) {
     // Workgroups that fit a compute unit (LDS and registers) in either pass.
     const bool bf = e == Elem::BF16;
     const double fit_first = bf ? (p.dstate <= 160 ? 4 : 2) : p.dstate <= 96 ? 2 : 1;
-    const double fit_second = p.dstate <= (bf ? 160 : 32) ? 2 : 1;
+    const double fit_second = p.dstate <= (bf ? 160 : 96) ? 2 : 1;
     auto rounds = [](double wgs, double fit) {
         const double each = ceil(wgs / 256.0), whole = floor(each / fit), rest = each - whole * fit;
         return whole * (0.25 + 0.75 * fit) + (rest > 0.0 ? 0.25 + 0.75 * rest : 0.0);
