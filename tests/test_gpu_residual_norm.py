@@ -98,6 +98,18 @@ def test_in_place(dim, dtype, stream):
         assert h is None and torch.equal(out, want[0])
 
 
+@pytest.mark.parametrize("dim", [64, 1001, 40000])
+def test_outputs_at_odd_addresses(dim):
+    s = inputs(31, (2, 5, dim), "bf16", "bf16", True, "token", "silu", True)
+    out, h = ssd.ssd_residual_norm_fwd(**s)
+    rooms = [torch.full((out.numel() + 2,), 7.0, dtype=out.dtype, device="cuda") for _ in range(2)]
+    got = [r[1:-1].view(out.shape) for r in rooms]
+    ssd.ssd_residual_norm_fwd(**s, out=got[0], residual_out=got[1])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], out) and torch.equal(got[1], h)
+    assert all(r[0] == 7 and r[-1] == 7 for r in rooms)
+
+
 def test_without_residual_the_stream_takes_the_given_type():
     s = inputs(3, (2, 5, 96), "bf16", "bf16", True, None, None, False, res=False)
     h = torch.empty(2, 5, 96, device="cuda")
