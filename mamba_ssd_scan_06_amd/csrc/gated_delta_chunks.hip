@@ -25,15 +25,13 @@
 // States, X and U are fp32 and enter the products as sums of bf16 terms: three
 // hold all 24 bits of the fraction, and of the products of two such sums those
 // below 2^-24 of the first are left out.  bf16 inputs are one term, fp32 ones
-// three.  Where the result is only rounded to a bf16 output (S q and Pm U of bf16
-// calls), two terms (16 bits) are taken: 2^-16 beside the output's 2^-8.  This is
-// 3 to 6 products of the bf16 rate, which is 16 times the fp32 rate.
+// three.  This is 3 to 6 products of the bf16 rate, which is 16 times the fp32
+// rate.  Tb X and Pm U of bf16 calls, where neither side is a bf16 input, are fp32
+// products instead: twice the matrix cores' time of six products of terms, but no
+// vector instructions for X's and U's terms, and two thirds of the tables' bytes.
 //
-// 8 x 2048 tokens of 32 heads (N and P 128, 8 groups, bf16) take 225 us: the
-// preparation 44, bound by its 213 MB of reads and tables (4.8 TB/s), the chunks
-// 180, in which the matrix cores are 59% busy with 104 products per wave and chunk
-// and the vector instructions (297) take most of the rest, since a SIMD hides only
-// about two of them behind each product.
+// 8 x 2048 tokens of 32 heads (N and P 128, 8 groups, bf16) take 237 us, most of
+// it in the chunks' matrix products and vector instructions.
 #include <math.h>
 
 #include "device_common.hpp"
@@ -51,15 +49,19 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_at2 __attribute__((aligned(2), may_alias));
 
 template <typename T> constexpr int kIn = sizeof(T) == 2 ? 1 : 3;   // terms of an input
-template <typename T> constexpr int kOut = sizeof(T) == 2 ? 2 : 3;  // terms of what an output is read from
 
-// What delta_prepare leaves per (sequence, chunk, head), in bytes: Tb by row
-// tile (the upper one needs the first 16 tokens only: half fragments) and term,
-// then Pm, then the tables.
+// What delta_prepare leaves per (sequence, chunk, head), in bytes: Tb, Pm, then
+// the tables.  bf16: Tb and Pm in fp32, tiles 00, 10 and 11, four values of each
+// per lane.  fp32: their terms, by row tile (the upper one needs the first 16
+// tokens only: half fragments) and term.
 template <typename T>
 struct Pack32 {
-    static constexpr int kT0 = 0, kT1 = kT0 + 3 * 64 * 8, kP0 = kT1 + 3 * 64 * 16, kP1 = kP0 + kOut<T> * 64 * 8,
-                         kTab = kP1 + kOut<T> * 64 * 16, kBytes = kTab + 512;
+    static constexpr bool kTerms = sizeof(T) == 4;
+    static constexpr int kValue = kTerms ? 6 : 4;  // bytes
+    static constexpr int kT0 = 0, kT1 = kT0 + 64 * 4 * kValue, kP0 = kT1 + 64 * 8 * kValue, kP1 = kP0 + 64 * 4 * kValue,
+                         kTab = kP1 + 64 * 8 * kValue, kUsed = kTab + 512;
+    // The direct copies' two instructions of 1 KB per wave.
+    static constexpr int kBytes = kTerms ? kUsed : 8 * 1024;
     // floats of the tables
     static constexpr int kA = 0, kC = 32, kD = 64, kEnd = 96;
 };
@@ -333,25 +335,31 @@ __global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
         for (int k = 0; k < 3; ++k)
 #pragma unroll
             for (int r = 0; r < 4; ++r) tv[k][r] = tt[k][r] * bj[k / 2][r];
-        auto put = [&](const float (&lo)[4], const float (&hi)[4], int off, auto terms) {
-            constexpr int N = decltype(terms)::value;
+        [[maybe_unused]] auto put = [&](const float (&lo)[4], const float (&hi)[4], int off) {
             const float both[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            bf16x8 f[N];
+            bf16x8 f[3];
             split(both, f);
 #pragma unroll
-            for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x8 *>(out + off + (k * 64 + lane) * 16) = f[k];
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8 *>(out + off + (k * 64 + lane) * 16) = f[k];
         };
-        auto put_half = [&](const float (&v)[4], int off, auto terms) {
-            constexpr int N = decltype(terms)::value;
-            bf16x4 f[N];
+        [[maybe_unused]] auto put_half = [&](const float (&v)[4], int off) {
+            bf16x4 f[3];
             split(v, f);
 #pragma unroll
-            for (int k = 0; k < N; ++k) *reinterpret_cast<bf16x4 *>(out + off + (k * 64 + lane) * 8) = f[k];
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x4 *>(out + off + (k * 64 + lane) * 8) = f[k];
         };
-        put_half(tv[0], L::kT0, std::integral_constant<int, 3>{});
-        put(tv[1], tv[2], L::kT1, std::integral_constant<int, 3>{});
-        put_half(pm[0], L::kP0, std::integral_constant<int, kOut<T>>{});
-        put(pm[1], pm[2], L::kP1, std::integral_constant<int, kOut<T>>{});
+        if constexpr (L::kTerms) {
+            put_half(tv[0], L::kT0);
+            put(tv[1], tv[2], L::kT1);
+            put_half(pm[0], L::kP0);
+            put(pm[1], pm[2], L::kP1);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                *reinterpret_cast<f32x4 *>(out + L::kT0 + (k * 64 + lane) * 16) = f32x4{tv[k][0], tv[k][1], tv[k][2], tv[k][3]};
+                *reinterpret_cast<f32x4 *>(out + L::kP0 + (k * 64 + lane) * 16) = f32x4{pm[k][0], pm[k][1], pm[k][2], pm[k][3]};
+            }
+        }
         float *tab = reinterpret_cast<float *>(out + L::kTab);
         if (lane < C) {
             const TwoFloats zero = {0.f, 0.f}, end = {w.hi[C - 1], w.lo[C - 1]};
@@ -431,7 +439,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
     typedef Pack32<T> L;
     typedef Buffer<T, NB, OUT> Buf;
     typedef Carry<T, NB, OUT> Regs;
-    constexpr int NI = kIn<T>, NO = kOut<T>;
+    constexpr int NI = kIn<T>;
     static_assert(!DIRECT || (sizeof(T) == 2 && BUFS == 2 && L::kBytes == 8 * 1024), "direct copies");
     // Two objects, so that the compiler knows reads of one apart from the copies
     // into the other and does not make them wait.
@@ -516,7 +524,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             copy(v_next, map ? 0u : bytes(p.v_ts, v_cols), v_off, &to.v[0][0] + 512 * uwave);
         } else {
             const int at = 1024 * (4 * (k - kKeySteps - 1) + uwave);
-            copy(pack_next, left_next > 0 ? (uint32_t)L::kBytes : 0u, (uint32_t)at + 16u * lane, to.pack + at);
+            copy(pack_next, left_next > 0 ? (uint32_t)L::kUsed : 0u, (uint32_t)at + 16u * lane, to.pack + at);
         }
     };
     auto advance = [&]() __attribute__((always_inline)) {
@@ -571,7 +579,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 #pragma unroll
             for (int i = 0; i < Regs::kPackWords; ++i) {
                 const int at = 16 * (kThreads * i + 64 * wave);
-                if (at + 1024 <= L::kBytes || at + 16 * lane < L::kBytes) copy16_to_lds(src + at + 16 * lane, to.pack + at);
+                if (at + 1024 <= L::kUsed || at + 16 * lane < L::kUsed) copy16_to_lds(src + at + 16 * lane, to.pack + at);
             }
         } else {
 #pragma unroll
@@ -751,7 +759,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             };
             // S k (rows: tokens); the terms of S are kept for S q (rows: p).
             f32x4 ks[2] = {};
-            bf16x8 sf[NB][AHEAD ? 3 : NO], kf[2][2][NI], qf[2][2][NI];
+            bf16x8 sf[NB][3], kf[2][2][NI], qf[2][2][NI];
             auto split_state = [&](int kb) { split_tiles(s[kb], sf[kb]); };
             rows_of(buf.k, 0, kf[0]);
             if constexpr (AHEAD) split_state(0);
@@ -769,12 +777,9 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                     float f[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) f[i] = s[kb][i >> 2][i & 3];
-                    bf16x8 st[3];
-                    split(f, st);
+                    split(f, sf[kb]);
 #pragma unroll
-                    for (int e = 0; e < NO; ++e) sf[kb][e] = st[e];
-#pragma unroll
-                    for (int I = 0; I < 2; ++I) mma_terms<NI, 3>(kf[kb & 1][I], st, ks[I]);
+                    for (int I = 0; I < 2; ++I) mma_terms<NI, 3>(kf[kb & 1][I], sf[kb], ks[I]);
                 }
             }
             auto s_q = [&](int kb) {
@@ -784,7 +789,7 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                 __builtin_amdgcn_sched_barrier(0);
                 if (OUT)
 #pragma unroll
-                    for (int I = 0; I < 2; ++I) mma_terms<NO, NI>(sf[kb], qf[kb & 1][I], qs[I]);
+                    for (int I = 0; I < 2; ++I) mma_terms<3, NI>(sf[kb], qf[kb & 1][I], qs[I]);
             };
             // X = v - a S k.
             f32x4 av[2];
@@ -806,31 +811,44 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = fmaf(-av[i >> 2][i & 3], ks[i >> 2][i & 3], x[i]);
             // U = Tb X.
-            bf16x4 t0[3], x0[3];
-            bf16x8 t1[3], xf[3];
+            [[maybe_unused]] f32x4 tt[3];
+            [[maybe_unused]] bf16x4 t0[3];
+            [[maybe_unused]] bf16x8 t1[3];
+            auto tables = [&](int off0, int off1, f32x4 (&tiles)[3], bf16x4 (&half)[3], bf16x8 (&both)[3]) {
 #pragma unroll
-            for (int e = 0; e < 3; ++e) {
-                t0[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + L::kT0 + (e * 64 + lane) * 8);
-                t1[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + L::kT1 + (e * 64 + lane) * 16);
-            }
+                for (int e = 0; e < 3; ++e)
+                    if constexpr (L::kTerms) {
+                        half[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + off0 + (e * 64 + lane) * 8);
+                        both[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + off1 + (e * 64 + lane) * 16);
+                    } else {
+                        tiles[e] = *reinterpret_cast<const f32x4 *>(buf.pack + off0 + (e * 64 + lane) * 16);
+                    }
+            };
+            tables(L::kT0, L::kT1, tt, t0, t1);
             if (NB > 1) s_q(1);
             else __builtin_amdgcn_sched_barrier(0);
-            split(x, xf);  // the chain waits for this one
-#pragma unroll
-            for (int e = 0; e < 3; ++e) x0[e] = bf16x4{xf[e][0], xf[e][1], xf[e][2], xf[e][3]};
             f32x4 u[2] = {}, dv[2];
-            mma_terms<3, 3>(t0, x0, u[0]);
-            mma_terms<3, 3>(t1, xf, u[1]);
+            if constexpr (L::kTerms) {
+                bf16x4 x0[3];
+                bf16x8 xf[3];
+                split(x, xf);  // the chain waits for this one
+#pragma unroll
+                for (int e = 0; e < 3; ++e) x0[e] = bf16x4{xf[e][0], xf[e][1], xf[e][2], xf[e][3]};
+                mma_terms<3, 3>(t0, x0, u[0]);
+                mma_terms<3, 3>(t1, xf, u[1]);
+            } else {
+                const f32x4 xt[2] = {{x[0], x[1], x[2], x[3]}, {x[4], x[5], x[6], x[7]}};
+                u[0] = mma_f32_16(tt[0], xt[0], u[0]);
+                u[1] = mma_f32_16(tt[1], xt[0], u[1]);
+                u[1] = mma_f32_16(tt[2], xt[1], u[1]);
+            }
 #pragma unroll
             for (int kb = 2; kb < NB; ++kb) s_q(kb);
-            bf16x8 p1[NO];
-            bf16x4 pm0[NO];
+            [[maybe_unused]] f32x4 pm[3];
+            [[maybe_unused]] bf16x4 pm0[3];
+            [[maybe_unused]] bf16x8 pm1[3];
+            tables(L::kP0, L::kP1, pm, pm0, pm1);
             float cv[2];
-#pragma unroll
-            for (int e = 0; e < NO; ++e) {
-                pm0[e] = *reinterpret_cast<const bf16x4 *>(buf.pack + L::kP0 + (e * 64 + lane) * 8);
-                p1[e] = *reinterpret_cast<const bf16x8 *>(buf.pack + L::kP1 + (e * 64 + lane) * 16);
-            }
 #pragma unroll
             for (int I = 0; I < 2; ++I) {
                 cv[I] = tab[L::kC + 16 * I + i16];
@@ -858,6 +876,27 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
                         mma_terms<NI, 3>(kt, uf, m[kb][half]);
                     }
                 store_state(m, p.state_out + bh * v_state);
+            }
+            // y: rows p = p0 + 4 g + r, column: token 16 I + i16.
+            if constexpr (OUT) {
+#pragma unroll
+                for (int I = 0; I < 2; ++I)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) qs[I][r] *= cv[I];
+                if constexpr (L::kTerms) {
+                    const float uv[8] = {u[0][0], u[0][1], u[0][2], u[0][3], u[1][0], u[1][1], u[1][2], u[1][3]};
+                    bf16x8 uf[3];
+                    bf16x4 u0[3];
+                    split_values(uv, uf);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) u0[e] = bf16x4{uf[e][0], uf[e][1], uf[e][2], uf[e][3]};
+                    mma_terms<3, 3>(u0, pm0, qs[0]);
+                    mma_terms<3, 3>(uf, pm1, qs[1]);
+                } else {
+                    qs[0] = mma_f32_16(u[0], pm[0], qs[0]);
+                    qs[1] = mma_f32_16(u[0], pm[1], qs[1]);
+                    qs[1] = mma_f32_16(u[1], pm[2], qs[1]);
+                }
             }
             // The state after the chunk.
             {
@@ -890,23 +929,6 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
 #pragma unroll
                             for (int e = 0; e < NI; ++e) kt[half][e] = next[half][e];
                 }
-            }
-            // y: rows p = p0 + 4 g + r, column: token 16 I + i16.
-            if constexpr (OUT) {
-                float uv[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) uv[i] = u[i >> 2][i & 3];
-                bf16x8 uf[NO];
-                bf16x4 u0[NO];
-                split_values(uv, uf);
-#pragma unroll
-                for (int e = 0; e < NO; ++e) u0[e] = bf16x4{uf[e][0], uf[e][1], uf[e][2], uf[e][3]};
-#pragma unroll
-                for (int I = 0; I < 2; ++I)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) qs[I][r] *= cv[I];
-                mma_terms<NO, NO>(u0, pm0, qs[0]);
-                mma_terms<NO, NO>(uf, p1, qs[1]);
             }
         }
         // The loads of the next chunk are waited for before the outputs are
