@@ -525,9 +525,10 @@ typedef struct {
  *   q, k          [b,T,G,N]  dtype  strided by batch and token; a token's G*N
  *                                   values are contiguous
  *   v             [b,T,H,P]  dtype  strided like them
- *   g             [b,T,H]    fp32   log decays (<= 0; greater ones are computed
- *                                   as given), strided by batch and token;
- *                                   NULL = 0 (no decay)
+ *   g             [b,T,H]    fp32   log decays, <= 0 down to -inf (which empties
+ *                                   the state; greater ones are computed as given
+ *                                   while sums over 32 tokens stay below 80),
+ *                                   strided by batch and token; NULL = 0 (no decay)
  *   beta          [b,T,H]    fp32   strided like g
  *   init_state    [b,H,P,N]  fp32   NULL = zeros
  *   y             [b,T,H,P]  dtype  dense, rounded once from fp32
@@ -537,10 +538,12 @@ typedef struct {
  *                                   non-NULL exactly when state_out_idx is
  *   workspace     16-byte aligned, ssd_gated_delta_workspace_bytes(...) bytes,
  *                 contents on entry ignored; may be NULL when that is 0
- * States are fp32 throughout and 16-byte aligned.  Values are finite, those of
- * padding tokens too (products over whole chunks read them); g and beta need not
- * be bounded, but keys of norm above sqrt(2 / beta) make the rule itself grow.  A few tokens run token by token, prompts in chunks (this needs
- * the workspace); the choice depends on the sizes and dtype alone.  With a
+ * States are fp32 throughout and 16-byte aligned.  Values but those of g are
+ * finite, and so are in fp32 the squares of q's and k's norms and the states that
+ * the rule makes, padding tokens included: a chunk's products read all of its
+ * tokens.  Keys of norm above sqrt(2 / beta) make the rule itself grow.  A few
+ * tokens run token by token, prompts in chunks (this needs the workspace); the
+ * choice depends on the sizes and dtype alone.  With a
  * padded batch, j_b = length - 1 gives each sequence's own state.
  * batch, nheads <= 65535, T < 2^31, batch * nheads * ceil(P / 32) < 2^24,
  * batch * nheads * ceil(T / 32) < 2^26. */

@@ -779,9 +779,9 @@ def ssd_gated_delta_fwd(q, k, v, g, beta, init_state=None, state_out_idx=None, *
     """Gated delta rule (see ssd_gated_delta_fwd in include/ssd.h).
 
     q, k [b,T,G,N] and v [b,T,H,P] bf16|fp32 (strides free by batch and token,
-    e.g. the convolution's outputs), g [b,T,H] fp32 log decays or None for
-    none, beta [b,T,H] fp32 (strides free as well), init_state [b,H,P,N] fp32
-    or None, state_out_idx [b] int32 or None; scale of the outputs, N ** -0.5
+    e.g. the convolution's outputs), g [b,T,H] fp32 log decays (-inf empties the
+    state) or None for none, beta [b,T,H] fp32 (strides free as well), init_state
+    [b,H,P,N] fp32 or None, state_out_idx [b] int32 or None; scale of the outputs, N ** -0.5
     when None; with qk_l2norm each q and k is normalised first.  Outputs and
     the workspace are allocated when not given; final_state may be init_state
     itself.  Returns (y, final_state or None, state_out or None).  Errors as

@@ -67,6 +67,13 @@ struct Pack32 {
 };
 constexpr int kAtFloats = 36;  // the accepted index's weights [32] and decay, per (sequence, head)
 
+// The least log decay that enters the sums of a chunk.  Its exponential is 0 (of
+// anything below -104), and so is that of any sum with it unless more than 65000
+// follows; but sums of 32 stay below 2^22 (times log2 e), where two floats, and the
+// double before them, hold the differences of later tokens to 2^-27.  Without it
+// -1e14 would swallow the decays after it, and an infinity make them NaN.
+constexpr float kLeastDecay = -65536.0f;
+
 // A sum of log decays in two floats, its rounding and what that left: sums of a
 // chunk may be large where their differences are small.
 struct TwoFloats {
@@ -76,8 +83,9 @@ __device__ __forceinline__ TwoFloats two_floats(double v) {
     const float hi = (float)v;
     return {hi, (float)(v - (double)hi)};
 }
-// 2^(a - b): off by |a - b| 2^-24 of itself beside the hardware exponential's
-// unit, which is below 2^-24 absolutely where a <= b.
+// 2^(a - b), for sums below 2^22 in size: off by |a - b| 2^-24 and 2^-26 of itself
+// beside the hardware exponential's unit.  Where a <= b the first is below 2^-24
+// absolutely.
 __device__ __forceinline__ float exp2_diff(const TwoFloats &a, const TwoFloats &b) {
     return exp2_hw((a.hi - b.hi) + (a.lo - b.lo));
 }
@@ -213,6 +221,7 @@ __global__ __launch_bounds__(kThreads) void delta_prepare(DeltaParams p) {
         gt = bt = 0.0f;
         if (lane < left) {
             if (p.g) gt = p.g[b * p.g_bs + (t0 + lane) * p.g_ts + h];
+            gt = gt < kLeastDecay ? kLeastDecay : gt;  // a NaN stays one
             bt = p.beta[b * p.beta_bs + (t0 + lane) * p.beta_ts + h];
         }
     };
