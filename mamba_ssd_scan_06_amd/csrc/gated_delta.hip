@@ -174,9 +174,16 @@ hipError_t launch(const DeltaParams &p, hipStream_t stream) {
     // 14.0, 27.3 and 101 us with one, 15.2, 21.9 and 90 with two.  N beyond 160 has
     // too many registers (256, 16 heads, 16 tokens of 32 sequences: 129 and 142);
     // for 2 tokens of 64 sequences only the states' traffic counts, which more waves
-    // carry better (70 and 75; 16 sequences 18.6 and 16.7).
-    const int64_t pairs = p.batch * p.nheads * ((p.headdim + 2 * kRows - 1) / (2 * kRows));
-    const bool two = M <= 5 && pairs >= 1024 && (p.seqlen >= 4 || pairs < 4096);
+    // carry better (70 and 75; 16 sequences 18.6 and 16.7).  Rows that 64 leave empty
+    // cost as much as others: N 128, 9 tokens of 64 sequences, P 16 and 32 24.0 and
+    // 25.7 us with one, 30.2 and 32.1 with two, P 80 and 96 68 and 70, 72 and 74, but
+    // P 48 50 and 36, P 144 and 160 107 and 101.  So never where they are half, and
+    // up to a quarter, or a third where the workgroups are few (P 80, 16 sequences
+    // 20.8 and 18.8).
+    const int slices = (p.headdim + kRows - 1) / kRows, wide = (p.headdim + 2 * kRows - 1) / (2 * kRows);
+    const int64_t pairs = p.batch * p.nheads * wide;
+    const bool fills = slices > 1 && (8 * wide <= 5 * slices || pairs < 2048);
+    const bool two = M <= 5 && fills && pairs >= 1024 && (p.seqlen >= 4 || pairs < 4096);
     const int rows = two ? 2 * kRows : kRows;
     const unsigned grid = (unsigned)(p.batch * p.nheads * ((p.headdim + rows - 1) / rows));
     if constexpr (M <= 5)
