@@ -1124,17 +1124,23 @@ hipError_t run(const DeltaParams &p, hipStream_t stream) {
 // ranges: 799, 751, 525, 472, 486, 455, 461, 498 and 491 us; 1021 tokens of 30
 // heads (N 96, P 80, fp32) in 1, 2, 3, 4, 5 and 6: 105, 97, 77, 71, 89 and 93 us;
 // 32768 tokens of 8 heads in 1, 4, 8 and 16: 1535, 746, 411 and 293 us; 2 x 4096
-// tokens of 32 heads in 1, 2, 3 and 4: 215, 207, 212 and 210 us.
+// tokens of 32 heads in 1, 2, 3 and 4: 215, 207, 212 and 210 us.  Of 35 shapes (N 32
+// to 256, 8 to 32 heads, 2048 to 8192 tokens) the choice was within 7% of the best of
+// 12 numbers of ranges at 27, and 23% off at worst (2048 tokens of 16 heads, P 64, N
+// 128, fp32: 117 us in four, 95 in twelve).
 void delta_ranges(DeltaParams &p, Elem e) {
     p.ranges = 1;
     p.range_chunks = p.nchunks;
     if (p.nchunks < 2) return;
     const double heads = (double)p.batch * p.nheads;
     const int v_slices = (p.headdim + kSlice - 1) / kSlice, n_slices = (p.dstate + kSlice - 1) / kSlice;
-    // Workgroups that fit a compute unit (LDS and registers) in either pass.
-    const bool bf = e == Elem::BF16;
-    const double fit_first = bf ? (p.dstate <= 160 ? 4 : 2) : p.dstate <= 96 ? 2 : 1;
-    const double fit_second = p.dstate <= (bf ? 160 : 96) ? 2 : 1;
+    // Workgroups that fit a compute unit in either pass, by ceil(N / 32): LDS and the
+    // registers of the compiled instances (bf16: of direct copies; rows that pass
+    // through registers leave up to two fewer, with which the choice is no better).
+    static constexpr int kFit[2][2][8] = {{{3, 2, 2, 1, 1, 1, 1, 1}, {2, 2, 2, 1, 1, 1, 1, 1}},   // fp32
+                                          {{5, 5, 4, 4, 3, 2, 2, 2}, {4, 4, 3, 2, 2, 1, 1, 1}}};  // bf16
+    const int nb = (p.dstate + 31) / 32 - 1;
+    const double fit_first = kFit[e == Elem::BF16][0][nb], fit_second = kFit[e == Elem::BF16][1][nb];
     auto rounds = [](double wgs, double fit) {
         const double each = ceil(wgs / 256.0), whole = floor(each / fit), rest = each - whole * fit;
         return whole * (0.25 + 0.75 * fit) + (rest > 0.0 ? 0.25 + 0.75 * rest : 0.0);
