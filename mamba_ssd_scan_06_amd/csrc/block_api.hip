@@ -17,9 +17,11 @@ using ssd::Range;
 using ssd::range;
 
 // Calls of more tokens run in chunks.  N and P 128, 32 heads, token by token and in
-// chunks: bf16, 16 tokens of 1 and 64 sequences 14.3 / 14.2 and 117 / 114 us, 24
-// tokens 19.5 / 14.4 and 151 / 116; fp32, whose chunks cost twice as much, 24 tokens
-// 18.1 / 20.7 and 148 / 214, 32 tokens 22.7 / 20.9 and 182 / 221.
+// chunks: bf16, 16 tokens of 1, 8 and 64 sequences 13.8 / 12.9, 17.9 / 19.1 and 108 /
+// 82 us (118 / 114 with an accepted state), 12 tokens 11.6 / 12.7, 15.6 / 18.9 and 90 /
+// 81 (100 / 112), 24 tokens 19.0 / 13.2, 24.0 / 19.4 and 143 / 85 (153 / 118); fp32,
+// whose chunks cost twice as much, 24 tokens 17.8 / 19.3, 23.6 / 30.9 and 136 / 178 (150
+// / 215), 32 tokens 22.4 / 20.0, 30.4 / 32.0 and 171 / 185.
 int64_t delta_tokens(ssd_dtype dtype) { return dtype == SSD_DTYPE_BF16 ? 16 : 24; }
 
 ssd_status check_delta(const ssd_delta_shape *s, ssd_dtype dtype) {

@@ -7,6 +7,9 @@
 // (another type, shape, layout or device, a CPU tensor) returns None, and the
 // binding's own code then refuses the call or makes it.  A status other than
 // SSD_OK comes back as an int.
+//
+// Built against a ROCm build of torch (libtorch_hip): allocations go straight to
+// its allocator of GPU memory.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -30,8 +30,11 @@
 // products instead: twice the matrix cores' time of six products of terms, but no
 // vector instructions for X's and U's terms, and two thirds of the tables' bytes.
 //
-// 8 x 2048 tokens of 32 heads (N and P 128, 8 groups, bf16) take 237 us, most of
-// it in the chunks' matrix products and vector instructions.
+// 8 x 2048 tokens of 32 heads (N and P 128, 8 groups, bf16) take 237 us: the
+// preparation 40, bound by its 186 MB of reads and tables (4.6 TB/s), the chunks
+// 196, in which the matrix cores are 66% busy with 116 products per wave and chunk
+// (24 of them fp32, of twice the cycles) and the vector instructions (257) 30%.  The
+// two hardly overlap: both waves of a SIMD walk the same phases.
 #include <math.h>
 
 #include "device_common.hpp"
@@ -91,7 +94,7 @@ __device__ __forceinline__ float exp2_diff(const TwoFloats &a, const TwoFloats &
 }
 
 // v as a sum of N bf16 terms, each the next 8 bits of the fraction (cut off, so
-// that three terms are v itself and two leave less than 2^-15 of it).  A pair of
+// that three terms are v itself).  A pair of
 // values takes one byte permutation per term and an and and a subtraction per
 // value between terms; rounding with v_cvt_pk_bf16_f32 costs as many and half of
 // them at twice the time.
@@ -722,8 +725,8 @@ __global__ __launch_bounds__(kThreads, WAVES) void delta_chunks(DeltaParams p) {
             // What a term leaves of the state or of the updates is a product of the
             // matrix cores too: the tile minus the unit matrix times the term, exact, in
             // the place of two vector instructions per value, which such a wave is bound
-            // by (16384 tokens of 32 heads in one range 861 -> 799 us with the state's;
-            // 2 x 4096 tokens 207 -> 202 with the updates').  The state's terms are taken
+            // by (7% of the time of 16384 tokens of 32 heads in one range with the state's,
+            // 2% of 2 x 4096 tokens with the updates').  The state's terms are taken
             // a step ahead, so that nothing waits for them; where the registers do not
             // hold that, or a lone wave per SIMD would wait, they are subtracted.
             constexpr bool AHEAD = WAVES == 2 && (NB <= 4 || DIRECT);
@@ -1121,10 +1124,10 @@ hipError_t run(const DeltaParams &p, hipStream_t stream) {
 // to be filled; the first pass computes no outputs (0.65), and its workgroups are
 // more (the maps' rows); the launches and the join add about 2 + r.  Measured,
 // 16384 tokens of 32 heads (N and P 128, bf16) in 1, 2, 3, 4, 5, 7, 8, 10 and 16
-// ranges: 799, 751, 525, 472, 486, 455, 461, 498 and 491 us; 1021 tokens of 30
-// heads (N 96, P 80, fp32) in 1, 2, 3, 4, 5 and 6: 105, 97, 77, 71, 89 and 93 us;
-// 32768 tokens of 8 heads in 1, 4, 8 and 16: 1535, 746, 411 and 293 us; 2 x 4096
-// tokens of 32 heads in 1, 2, 3 and 4: 215, 207, 212 and 210 us.  Of 35 shapes (N 32
+// ranges: 876, 775, 541, 492, 506, 457, 460, 509 and 494 us; 1021 tokens of 30
+// heads (N 96, P 80, fp32) in 1, 2, 3, 4, 5 and 6: 107, 97, 77, 72, 76 and 81 us;
+// 32768 tokens of 8 heads in 1, 4, 8 and 16: 1696, 769, 424 and 298 us; 2 x 4096
+// tokens of 32 heads in 1, 2, 3 and 4: 235, 213, 223 and 214 us.  Of 35 shapes (N 32
 // to 256, 8 to 32 heads, 2048 to 8192 tokens) the choice was within 7% of the best of
 // 12 numbers of ranges at 27, and 23% off at worst (2048 tokens of 16 heads, P 64, N
 // 128, fp32: 117 us in four, 95 in twelve).
